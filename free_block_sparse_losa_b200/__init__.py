@@ -14,6 +14,8 @@ __all__ = ["LosaShape", "LosaError", "make_shape", "losa_dense_profile", "losa_s
            "losa_select_topk", "losa_sparse_attn",
            "losa_select_workspace_bytes", "losa_get_device_error", "losa_selftest_wait_timeout",
            "losa_set_wait_limit_ns", "losa_status_string", "losa_version", "library_path", "load",
+           "LosaRope", "LosaCache", "LosaTokenView", "make_rope", "make_cache", "losa_rope_apply", "losa_cache_append",
+           "losa_cache_attn", "losa_cache_attn_workspace_bytes",
            "DTYPE_F32", "DTYPE_BF16", "STATUS"]
 
 DTYPE_F32 = 0
@@ -35,6 +37,33 @@ class LosaShape(ctypes.Structure):
     _fields_ = [("heads", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("n_padded", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("block_q", ctypes.c_int32), ("block_k", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class LosaRope(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("axis_dims", ctypes.c_int32 * 3), ("grid_y", ctypes.c_int32),
+                ("grid_x", ctypes.c_int32), ("offset", ctypes.c_int32 * 3), ("pairing", ctypes.c_int32),
+                ("theta", ctypes.c_double)]
+
+
+class LosaCache(ctypes.Structure):
+    _fields_ = [("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("seqs", ctypes.c_int32), ("table_stride", ctypes.c_int32)]
+
+
+class LosaTokenView(ctypes.Structure):
+    _fields_ = [("parts", ctypes.c_int32), ("batch", ctypes.c_int32), ("tokens", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("part_stride", ctypes.c_int64), ("batch_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+def make_rope(head_dim, axis_dims, grid, offset=(0, 0, 0), theta=10000.0, halves=False) -> LosaRope:
+    """Rotary positions with three axes: rotated dimensions per axis (t, y, x) and the token grid's (y, x) extents."""
+    return LosaRope(head_dim, (ctypes.c_int32 * 3)(*axis_dims), grid[0], grid[1], (ctypes.c_int32 * 3)(*offset),
+                    1 if halves else 0, theta)
+
+
+def make_cache(kv_heads, head_dim, page_tokens, n_pages, seqs, table_stride) -> LosaCache:
+    return LosaCache(kv_heads, head_dim, page_tokens, n_pages, seqs, table_stride)
 
 
 def make_shape(heads, n_tokens, n_padded, head_dim, block_q, block_k, dtype) -> LosaShape:
@@ -69,6 +98,13 @@ def load():
     L.losa_select_workspace_bytes.argtypes = [sp]
     L.losa_select_workspace_bytes.restype = sz
     L.losa_sparse_attn.argtypes = [sp, vp, vp, vp, f32, vp, vp, vp, vp, vp, vp]
+    rp, cp, tp = ctypes.POINTER(LosaRope), ctypes.POINTER(LosaCache), ctypes.POINTER(LosaTokenView)
+    L.losa_rope_apply.argtypes = [rp, i32, tp, vp, tp, vp, ctypes.c_uint32, i32, vp, vp, vp]
+    L.losa_cache_append.argtypes = [cp, rp, i32, vp, i64, i64, vp, i64, i64, i64, i32] + [vp] * 10
+    L.losa_cache_attn.argtypes = ([cp, i32, i32, i32, vp, i64, i64, i64] + [vp] * 6 + [f32, i32, vp, i64, i64, i64] +
+                                  [vp, vp, sz, vp])
+    L.losa_cache_attn_workspace_bytes.argtypes = [cp, i32, i32, i32]
+    L.losa_cache_attn_workspace_bytes.restype = sz
     L.losa_get_device_error.argtypes = [vp]
     L.losa_selftest_wait_timeout.argtypes = [ctypes.c_uint32, vp]
     L.losa_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
@@ -77,7 +113,7 @@ def load():
     L.losa_status_string.restype = ctypes.c_char_p
     L.losa_version.restype = ctypes.c_int
     for name in ("losa_dense_profile", "losa_dense_profile_ws", "losa_select", "losa_select_noalloc", "losa_select_topk",
-                 "losa_sparse_attn",
+                 "losa_sparse_attn", "losa_rope_apply", "losa_cache_append", "losa_cache_attn",
                  "losa_get_device_error",
                  "losa_selftest_wait_timeout"):
         getattr(L, name).restype = i32
@@ -240,6 +276,106 @@ def losa_sparse_attn(shape, q, k, v, scale, indptr, kv_block_idx, order, o, lse=
     st = load().losa_sparse_attn(ctypes.byref(shape), pq, pk, pv, float(scale), pi, px, po, pout, pl,
                                  _stream(stream))
     return _check(st, "losa_sparse_attn", raise_on_error)
+
+
+def _strided(t, name, dtype, ndim):
+    """Device pointer of a tensor that may have any strides but a contiguous last dimension."""
+    import torch
+    if t.dtype != getattr(torch, dtype):
+        raise ValueError(f"{name}: expected torch.{dtype}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name}: expected {ndim} dimensions, got {t.dim()}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _on_device(*specs):
+    import torch
+    here = torch.cuda.current_device() if any(t.is_cuda for t, _ in specs) else None
+    for t, name in specs:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: expected a CUDA tensor")
+        if t.device.index != here:
+            raise ValueError(f"{name}: lives on {t.device}, the current device is cuda:{here}")
+
+
+_NAMES = {"torch.float32": ("float32", DTYPE_F32), "torch.bfloat16": ("bfloat16", DTYPE_BF16)}
+
+
+def _float_dtype(t, name):
+    got = _NAMES.get(str(t.dtype))
+    if got is None:
+        raise ValueError(f"{name}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
+    return got
+
+
+def losa_rope_apply(rope, x, y, rotate=1, inverse=False, positions=None, start=None, stream=None, raise_on_error=True):
+    """x, y: (parts, batch, tokens, heads, head_dim) views of any layouts (last dimension contiguous); y may hold more
+    tokens, which become zero rows. `rotate` is a bit mask of the parts that are rotated."""
+    dt, code = _float_dtype(x, "x")
+    px, py = _strided(x, "x", dt, 5), _strided(y, "y", dt, 5)
+    for t, name in ((x, "x"), (y, "y")):
+        if t.shape[4] != rope.head_dim:
+            raise ValueError(f"{name}: rows of {t.shape[4]}, the rotation is for {rope.head_dim}")
+    pp, ps = _ptrs((positions, "positions", "int32", 3 * x.shape[1] * x.shape[2]), (start, "start", "int32", x.shape[1]))
+    _on_device((x, "x"), (y, "y"))
+    xs, ys = x.stride(), y.stride()
+    xv = LosaTokenView(*x.shape[:4], *xs[:4])
+    yv = LosaTokenView(*y.shape[:4], *ys[:4])
+    st = load().losa_rope_apply(ctypes.byref(rope), code, ctypes.byref(xv), px, ctypes.byref(yv), py, int(rotate),
+                                int(bool(inverse)), pp, ps, _stream(stream))
+    return _check(st, "losa_rope_apply", raise_on_error)
+
+
+def _pool_ptrs(cache, k8, v8, k_scale, v_scale, page_table, lens):
+    n = max(cache.n_pages, 0) * max(cache.kv_heads, 0)
+    codes = n * max(cache.page_tokens, 0) * max(cache.head_dim, 0)
+    return _ptrs((k8, "k8", "float8_e4m3fn", codes), (v8, "v8", "float8_e4m3fn", codes),
+                 (k_scale, "k_scale", "float32", n), (v_scale, "v_scale", "float32", n),
+                 (page_table, "page_table", "int32", max(cache.seqs, 0) * max(cache.table_stride, 0)),
+                 (lens, "lens", "int32", cache.seqs))
+
+
+def losa_cache_append(cache, k, v, k8, v8, k_scale, v_scale, page_table, lens, new_tokens, indptr=None, new_lens=None,
+                      rope=None, positions=None, stream=None, raise_on_error=True):
+    """k, v: (tokens, kv_heads, head_dim) of all sequences' new tokens, strided alike or not."""
+    dt, code = _float_dtype(k, "k")
+    pk, pv = _strided(k, "k", dt, 3), _strided(v, "v", dt, 3)
+    for t, name in ((k, "k"), (v, "v")):
+        if tuple(t.shape) != (k.shape[0], cache.kv_heads, cache.head_dim):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (tokens, {cache.kv_heads}, {cache.head_dim})")
+    p8, pv8, pks, pvs, pt, pl = _pool_ptrs(cache, k8, v8, k_scale, v_scale, page_table, lens)
+    pi, pn, pp = _ptrs((indptr, "indptr", "int32", cache.seqs + 1), (new_lens, "new_lens", "int32", cache.seqs),
+                       (positions, "positions", "int32", 3 * k.shape[0]))
+    _on_device((k, "k"), (v, "v"))
+    st = load().losa_cache_append(ctypes.byref(cache), None if rope is None else ctypes.byref(rope), code, pk,
+                                  k.stride(0), k.stride(1), pv, v.stride(0), v.stride(1), k.shape[0], int(new_tokens),
+                                  pi, pp, pt, pl, pn, p8, pv8, pks, pvs, _stream(stream))
+    return _check(st, "losa_cache_append", raise_on_error)
+
+
+def losa_cache_attn_workspace_bytes(cache, heads, tokens, max_len=0) -> int:
+    return int(load().losa_cache_attn_workspace_bytes(ctypes.byref(cache), int(heads), int(tokens), int(max_len)))
+
+
+def losa_cache_attn(cache, q, k8, v8, k_scale, v_scale, page_table, lens, scale, o, lse=None, causal=True, max_len=0,
+                    workspace=None, stream=None, raise_on_error=True):
+    """q, o: (seqs, tokens, heads, head_dim) bf16, any strides but a contiguous last dimension; lse: (seqs, tokens,
+    heads). max_len bounds the lengths (0: the page table's capacity)."""
+    pq, po = _strided(q, "q", "bfloat16", 4), _strided(o, "o", "bfloat16", 4)
+    if q.shape[0] != cache.seqs or q.shape[3] != cache.head_dim or o.shape != q.shape:
+        raise ValueError(f"q, o: shapes {tuple(q.shape)}, {tuple(o.shape)}, expected ({cache.seqs}, tokens, heads, "
+                         f"{cache.head_dim}) of both")
+    p8, pv8, pks, pvs, pt, pl = _pool_ptrs(cache, k8, v8, k_scale, v_scale, page_table, lens)
+    pe, pw = _ptrs((lse, "lse", "float32", q.shape[0] * q.shape[1] * q.shape[2]), (workspace, "workspace", None, None))
+    _on_device((q, "q"), (o, "o"))
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    qs, os_ = q.stride(), o.stride()
+    st = load().losa_cache_attn(ctypes.byref(cache), q.shape[2], q.shape[1], int(bool(causal)), pq, qs[0], qs[1], qs[2],
+                                pt, pl, p8, pv8, pks, pvs, float(scale), int(max_len), po, os_[0], os_[1], os_[2], pe, pw,
+                                wsb, _stream(stream))
+    return _check(st, "losa_cache_attn", raise_on_error)
 
 
 def losa_get_device_error(stream=None) -> int:

@@ -23,7 +23,10 @@ constexpr unsigned int kDevErrBadData = 2u;
 #include "attn_tc.cuh"
 #include "attn_dense.cuh"
 #include "attn_sparse.cuh"
+#include "cache_append.cuh"
+#include "cache_attn.cuh"
 #include "ptx.cuh"
+#include "rope.cuh"
 #include "select.cuh"
 
 using namespace losa;
@@ -567,3 +570,5 @@ extern "C" losa_status losa_select_noalloc(const losa_shape* shape, const float*
     return run_select(shape, mass, tau, 0, indptr, kv_block_idx, idx_capacity, order, scratch, kNoAllocScratchBytes,
                       stream);
 }
+
+#include "cache_api.cuh"

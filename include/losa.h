@@ -182,6 +182,115 @@ losa_status losa_sparse_attn(const losa_shape* shape, const void* q, const void*
                              const int32_t* indptr, const int32_t* kv_block_idx, const int32_t* order, void* o,
                              float* lse, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------------------------------------------------
+ * Streaming: rotary positions, a paged 8-bit key/value cache, and attention over it.
+ *
+ * A clip generated chunk by chunk (or a few tokens at a time) keeps the keys and values of its earlier tokens. The calls
+ * below turn a projection's output into rotated tokens in any layout (losa_rope_apply), store keys and values in 8 bits
+ * with a scale per block of tokens and head (losa_cache_append), and attend to them for a few tokens (losa_cache_attn).
+ * The LoSA page has no counterpart: its blocks are the cache's pages.
+ * ------------------------------------------------------------------------------------------------------------------ */
+
+enum { LOSA_ROPE_INTERLEAVED = 0, LOSA_ROPE_HALVES = 1 };
+
+/* Rotary positions with three axes. The first axis_dims[0] dimensions of a row turn with t, the next axis_dims[1] with y,
+ * the next axis_dims[2] with x; what is left is not rotated. Within an axis of m dimensions pair i (0 <= i < m / 2) turns
+ * by pos * theta^(-2 i / m); it is made of dimensions (2i, 2i + 1) of the axis's section (interleaved) or (i, i + m / 2)
+ * (halves). Token n of the grid sits at t = n / (grid_y grid_x), y = (n / grid_x) mod grid_y, x = n mod grid_x, plus the
+ * offsets. Angles are exact to 2^-32 of a turn at any 32-bit position. */
+typedef struct {
+    int32_t head_dim;      /* d, at most 256; a row is a multiple of 16 bytes */
+    int32_t axis_dims[3];  /* even, their sum at most d                      */
+    int32_t grid_y, grid_x;
+    int32_t offset[3];     /* added to (t, y, x)                             */
+    int32_t pairing;       /* LOSA_ROPE_INTERLEAVED or LOSA_ROPE_HALVES      */
+    double theta;          /* finite, > 0                                    */
+} losa_rope;
+
+/* A token tensor in any layout: element (p, b, n, h, e) lies at p part_stride + b batch_stride + n token_stride +
+ * h head_stride + e. Parts are tensors that travel together (query, key and value of a fused projection). Strides are in
+ * elements, a multiple of 16 bytes; the stride of an extent of one does not matter. */
+typedef struct {
+    int32_t parts, batch, tokens, heads;
+    int64_t part_stride, batch_stride, token_stride, head_stride;
+} losa_token_view;
+
+/*
+ * y = R(position) x for the parts whose bit is set in `rotate`, y = x for the others, from x's layout into y's.
+ *   dtype     : LOSA_DTYPE_BF16 or LOSA_DTYPE_F32, of x and y; the arithmetic is fp32, rounded once.
+ *   x_view, y_view : the same parts, batch and heads; y may hold more tokens than x, and its rows behind them are set to
+ *               zero (the padded layout of the attention calls). y's strides must be at least d where an extent exceeds
+ *               one; x's may be zero (a broadcast input). x and y must not overlap.
+ *   inverse   : non-zero turns by the negative angles: R is orthogonal, so this is the gradient of the forward call
+ *               (with the two layouts exchanged), and with rotate = 0 the way back from head-major to token-major.
+ *   positions : [batch][tokens][3] int32 (t, y, x), or NULL for the grid.
+ *   start     : [batch] int32, the grid token that row 0 of a batch element is, or NULL for 0. Ignored with positions.
+ */
+losa_status losa_rope_apply(const losa_rope* rope, int32_t dtype, const losa_token_view* x_view, const void* x,
+                            const losa_token_view* y_view, void* y, uint32_t rotate, int32_t inverse,
+                            const int32_t* positions, const int32_t* start, cudaStream_t stream);
+
+/* A paged cache. The pool is k8, v8: [n_pages][kv_heads][page_tokens][head_dim] e4m3 codes and k_scale, v_scale:
+ * [n_pages][kv_heads] fp32; a code stands for code * scale. Sequence b's block j (tokens j page_tokens ...) is page
+ * page_table[b][j] (int32 [seqs][table_stride]) of the pool; its length is lens[b] (int32 [seqs]). head_dim is 64 or 128,
+ * page_tokens 32, 64 or 128 (else LOSA_ERR_UNSUPPORTED); n_pages * kv_heads * page_tokens must stay below 2^31. Scales are
+ * positive; losa_cache_append writes powers of two between 2^-40 and 2^60. */
+typedef struct {
+    int32_t kv_heads, head_dim, page_tokens, n_pages;
+    int32_t seqs, table_stride;
+} losa_cache;
+
+/*
+ * Appends new tokens to every sequence, rotating the keys on the way.
+ *   rope      : rotation of the keys, or NULL (keys are stored as they come). Without positions the token that becomes
+ *               number n of its sequence sits at grid token n.
+ *   dtype     : of k and v. Token i, head h of k starts at element i k_token_stride + h k_head_stride; likewise v. Strides
+ *               are multiples of 16 bytes.
+ *   total_tokens : tokens that k and v hold. Sequence b's new tokens are rows indptr[b] .. indptr[b + 1) (int32
+ *               [seqs + 1]), at most new_tokens of them, or, with indptr NULL, rows b new_tokens .. (b + 1) new_tokens.
+ *   positions : [total_tokens][3] int32 (t, y, x), or NULL.
+ *   lens      : lengths before the call; new_lens (may be NULL, must not be lens): lengths behind it.
+ * A block's scale is the smallest power of two 2^e with max |x| <= 448 * 2^e over its finite new values, -40 <= e <= 60,
+ * or the scale a part-full block already has if that is larger; where the scale grows, the block's held codes are rounded
+ * to it again. New values are rounded to nearest, infinities and values out of range saturate, NaN stays NaN. Nothing
+ * else of the pool is written: codes behind a sequence's last token keep what they hold.
+ * The pages a call writes must belong to one sequence each. A token count, length, row or page out of range sets the
+ * device error word (LOSA_ERR_DEVICE_FAULT); the tokens concerned are not stored.
+ */
+losa_status losa_cache_append(const losa_cache* cache, const losa_rope* rope, int32_t dtype, const void* k,
+                              int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                              int64_t v_head_stride, int64_t total_tokens, int32_t new_tokens, const int32_t* indptr,
+                              const int32_t* positions, const int32_t* page_table, const int32_t* lens,
+                              int32_t* new_lens, void* k8, void* v8, float* k_scale, float* v_scale,
+                              cudaStream_t stream);
+
+/*
+ * Attention of the last `tokens` tokens of every sequence over its whole cache (their own keys included: append first).
+ *   heads     : query heads, a multiple of kv_heads; query head h reads kv head h / (heads / kv_heads).
+ *   causal    : non-zero: token i of the `tokens` sees keys 0 .. lens[b] - tokens + i; zero: every key.
+ *   q, o      : bf16, element (b, i, h, e) at b seq_stride + i token_stride + h head_stride + e; strides are multiples of 8
+ *               elements. o must not overlap q.
+ *   scale     : logit scale, > 0.
+ *   max_len   : an upper bound of lens, by which the work is split; results do not depend on it being one. <= 0: the
+ *               table's capacity.
+ *   lse       : [seqs][tokens][heads] fp32 or NULL.
+ *   workspace : scratch of losa_cache_attn_workspace_bytes(cache, heads, tokens, max_len) bytes, 16-byte aligned (may be
+ *               NULL where that is 0), used during the call only; calls that can overlap need their own.
+ * A row that sees no key (an empty sequence) gets o = 0 and lse = -inf. Logits, weights' sums and O are fp32; weights
+ * are rounded to fp16 for the product with V. Codes of slots that hold no token are never used, whatever they are. A length
+ * outside [0, capacity] or a page out of range sets the device error word (LOSA_ERR_DEVICE_FAULT); the keys concerned
+ * are left out.
+ */
+losa_status losa_cache_attn(const losa_cache* cache, int32_t heads, int32_t tokens, int32_t causal, const void* q,
+                            int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
+                            const int32_t* page_table, const int32_t* lens, const void* k8, const void* v8,
+                            const float* k_scale, const float* v_scale, float scale, int32_t max_len, void* o,
+                            int64_t o_seq_stride, int64_t o_token_stride, int64_t o_head_stride, float* lse,
+                            void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Scratch bytes losa_cache_attn needs on the current device (0 where the keys are not split, or for bad arguments). */
+size_t losa_cache_attn_workspace_bytes(const losa_cache* cache, int32_t heads, int32_t tokens, int32_t max_len);
+
 /*
  * Synchronises `stream`, then returns and clears the current device's error word: LOSA_OK,
  * LOSA_ERR_DEVICE_FAULT, LOSA_ERR_TIMEOUT, or LOSA_ERR_CUDA if the synchronisation itself failed.
