@@ -15,7 +15,7 @@ __all__ = ["LosaShape", "LosaError", "make_shape", "losa_dense_profile", "losa_s
            "losa_select_workspace_bytes", "losa_get_device_error", "losa_selftest_wait_timeout",
            "losa_set_wait_limit_ns", "losa_status_string", "losa_version", "library_path", "load",
            "LosaRope", "LosaCache", "LosaTokenView", "make_rope", "make_cache", "losa_rope_apply", "losa_cache_append",
-           "losa_cache_attn", "losa_cache_attn_workspace_bytes",
+           "losa_cache_attn", "losa_cache_attn_workspace_bytes", "losa_cache_sparse_attn",
            "DTYPE_F32", "DTYPE_BF16", "STATUS"]
 
 DTYPE_F32 = 0
@@ -105,6 +105,7 @@ def load():
                                   [vp, vp, sz, vp])
     L.losa_cache_attn_workspace_bytes.argtypes = [cp, i32, i32, i32]
     L.losa_cache_attn_workspace_bytes.restype = sz
+    L.losa_cache_sparse_attn.argtypes = [sp, cp] + [vp] * 7 + [f32] + [vp] * 6
     L.losa_get_device_error.argtypes = [vp]
     L.losa_selftest_wait_timeout.argtypes = [ctypes.c_uint32, vp]
     L.losa_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
@@ -114,6 +115,7 @@ def load():
     L.losa_version.restype = ctypes.c_int
     for name in ("losa_dense_profile", "losa_dense_profile_ws", "losa_select", "losa_select_noalloc", "losa_select_topk",
                  "losa_sparse_attn", "losa_rope_apply", "losa_cache_append", "losa_cache_attn",
+                 "losa_cache_sparse_attn",
                  "losa_get_device_error",
                  "losa_selftest_wait_timeout"):
         getattr(L, name).restype = i32
@@ -376,6 +378,20 @@ def losa_cache_attn(cache, q, k8, v8, k_scale, v_scale, page_table, lens, scale,
                                 pt, pl, p8, pv8, pks, pvs, float(scale), int(max_len), po, os_[0], os_[1], os_[2], pe, pw,
                                 wsb, _stream(stream))
     return _check(st, "losa_cache_attn", raise_on_error)
+
+
+def losa_cache_sparse_attn(shape, cache, q, k8, v8, k_scale, v_scale, page_table, lens, scale, o, indptr=None,
+                           kv_block_idx=None, order=None, lse=None, stream=None, raise_on_error=True):
+    """losa_sparse_attn over the paged 8-bit cache; without lists every block of the sequence is attended to."""
+    H, Np, d, nq, _ = _dims(shape)
+    p8, pv8, pks, pvs, pt, pl = _pool_ptrs(cache, k8, v8, k_scale, v_scale, page_table, lens)
+    pq, pi, px, pr, po, pe = _ptrs(
+        (q, "q", "bfloat16", H * Np * d), (indptr, "indptr", "int32", H * nq + 1),
+        (kv_block_idx, "kv_block_idx", "int32", None), (order, "order", "int32", H * nq), (o, "o", "bfloat16", H * Np * d),
+        (lse, "lse", "float32", H * Np))
+    st = load().losa_cache_sparse_attn(ctypes.byref(shape), ctypes.byref(cache), pq, pt, pl, p8, pv8, pks, pvs,
+                                       float(scale), pi, px, pr, po, pe, _stream(stream))
+    return _check(st, "losa_cache_sparse_attn", raise_on_error)
 
 
 def losa_get_device_error(stream=None) -> int:

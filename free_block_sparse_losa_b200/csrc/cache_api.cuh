@@ -80,8 +80,8 @@ CacheGeom cache_geom(const losa_cache* c, const int32_t* table, const int32_t* l
 }
 
 // Tensor map over the pool's codes as a [pages * kv heads * page tokens][d] byte matrix, boxes of box_rows whole rows,
-// swizzled over the row (64 or 128 bytes).
-bool make_code_map(CUtensorMap* map, const losa_cache* c, const void* codes, uint32_t box_rows) {
+// swizzled over the row (64 or 128 bytes) or not.
+bool make_code_map(CUtensorMap* map, const losa_cache* c, const void* codes, uint32_t box_rows, bool swizzle = true) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t gdim[2] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->n_pages * c->kv_heads * c->page_tokens};
@@ -90,7 +90,8 @@ bool make_code_map(CUtensorMap* map, const losa_cache* c, const void* codes, uin
     const cuuint32_t estride[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), gdim, gstride, box, estride,
               CU_TENSOR_MAP_INTERLEAVE_NONE,
-              c->head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
+                       : (c->head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B),
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -345,6 +346,58 @@ losa_status losa_cache_attn(const losa_cache* cache, int32_t heads, int32_t toke
     a.wait_limit_ns = g_wait_limit_ns;
     return cache->head_dim == 128 ? launch_cache_attn<128>(cache, a, p, k8, v8, stream)
                                   : launch_cache_attn<64>(cache, a, p, k8, v8, stream);
+}
+
+losa_status losa_cache_sparse_attn(const losa_shape* shape, const losa_cache* cache, const void* q,
+                                   const int32_t* page_table, const int32_t* lens, const void* k8, const void* v8,
+                                   const float* k_scale, const float* v_scale, float scale, const int32_t* indptr,
+                                   const int32_t* kv_block_idx, const int32_t* order, void* o, float* lse,
+                                   cudaStream_t stream) {
+    const losa_status st = check_shape(shape);
+    if (st != LOSA_OK) return st;
+    if (!cache_ok(cache) || shape->head_dim != cache->head_dim || shape->block_k != cache->page_tokens ||
+        shape->heads % cache->seqs != 0 || (shape->heads / cache->seqs) % cache->kv_heads != 0)
+        return LOSA_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || !std::isfinite(scale) || (indptr == nullptr) != (kv_block_idx == nullptr))
+        return LOSA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(k8) || !aligned16(v8) || !aligned4(k_scale) || !aligned4(v_scale) ||
+        !aligned4(page_table) || !aligned4(lens) || (lse && !aligned16(lse)) || q == o)
+        return LOSA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(indptr) | reinterpret_cast<uintptr_t>(kv_block_idx) |
+         reinterpret_cast<uintptr_t>(order)) & 3u)
+        return LOSA_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)shape->heads * shape->n_padded;
+    if (shape->dtype != LOSA_DTYPE_BF16 || shape->head_dim != kTcDim || shape->block_q != kTcRows ||
+        !cache_supported(cache) || rows > 2147483647ll)
+        return LOSA_ERR_UNSUPPORTED;
+    CUtensorMap tk, tv, to;
+    if (!make_code_map(&tk, cache, k8, 32) || !make_code_map(&tv, cache, v8, 32, false) ||
+        !make_tile_map(&to, o, (uint64_t)rows))
+        return LOSA_ERR_CUDA;
+    CacheSparseArgs a;
+    a.g = cache_geom(cache, page_table, lens);
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.lse = lse;
+    a.heads = shape->heads / cache->seqs;
+    a.group = a.heads / cache->kv_heads;
+    a.Np = shape->n_padded;
+    a.nq = shape->n_padded / kTcRows;
+    a.n_items = shape->heads * a.nq;
+    a.sub = kTcRows / cache->page_tokens;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.indptr = indptr;
+    a.kv_idx = kv_block_idx;
+    a.order = order;
+    a.wait_limit_ns = g_wait_limit_ns;
+    const int sms = sm_count();
+    if (sms <= 0) return LOSA_ERR_CUDA;
+    if (cudaFuncSetAttribute(cache_sparse_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kCsSmem) !=
+        cudaSuccess)
+        return LOSA_ERR_CUDA;
+    cache_sparse_kernel<<<a.n_items < sms ? a.n_items : sms, kCsThreads, kCsSmem, stream>>>(tk, tv, to, a);
+    return launch_status();
 }
 
 }  // extern "C"

@@ -1,0 +1,681 @@
+// Attention of 128-row query blocks over listed blocks (or all blocks) of the paged 8-bit cache: cache_sparse_kernel.
+//
+// The mathematics is cache_attn.cuh's: with codes k, v and scales ks, vs of a block, x = c ks (q . k) + log2 vs, and O is the
+// sum of 2^(x - M) v over the sum of 2^(x - M) / vs, so no tile is ever scaled. Both products run on the tensor cores
+// without widening K: a bf16 query element has 8 significant bits and is split, after its row was brought to a largest
+// magnitude in [2^7, 2^8) by a power of two, into two e4m3 numbers of 4 bits each, q = q1 + q2 (exact down to 2^-9 of the
+// row's largest element, off by at most 2^-17 of it below), so Q K^T is two kind::f8f6f4 products that read the codes as
+// they lie in the cache, at the cost of one bf16 product. P keeps fp16's 11 bits and its range (weights down to 2^-31 of
+// the largest: the tail under an attention sink is not lost), so V is widened to fp16 on its way, which is exact; four
+// warps do that next to the softmax.
+//
+// One persistent CTA per SM walks one stream of items in rounds over the work order (a snake, longest first); the tiles
+// (128 keys: 1, 2 or 4 blocks) of all its items form one sequence n = 0, 1, 2, ...:
+//   warp 3       reads order, lists, page table and scales eight tiles at a time (a lane per 32-key quarter, so that the
+//                chain of dependent loads is paid once for eight tiles) into a ring of tile records.
+//   warp 0 / 2   TMA: K / V codes, four 32-key boxes a tile, one per lane.
+//   warps 12..15 split the next item's Q into shared memory one tile ahead, widen V (zeroing keys that do not exist), and
+//                store an item's O from the V slot it was staged in before refilling that slot.
+//   warp 1       MMA: S_n = Q K^T into S buffer n & 1, then O += P V of tile n - 1 with P from TMEM.
+//   warps 4..11  softmax in two warpgroups that split the tile's keys, as in attn_sparse.cuh.
+// TMEM: S_0 0..127, S_1 128..255, O 256..383, P_0 384..447, P_1 448..511. Buffer reuse follows attn_sparse.cuh: S buffer
+// n & 1 was read for tile n - 2 before its P, which the issuer has waited for; P buffer n & 1 was last read by P V of tile
+// n - 2, which completed before S_n in the in-order tensor pipe.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include "attn_tc.cuh"
+#include "cache_attn.cuh"
+
+namespace losa {
+
+constexpr int kCsThreads = 512;
+constexpr uint32_t kCsTile8 = 128 * 128;                  // a tile of codes
+constexpr int kCsKStages = 3;
+constexpr uint32_t kCsQ = 0;                              // 2 x (q1, q2)
+constexpr uint32_t kCsK = 4 * kCsTile8;                   // 3 K tiles
+constexpr uint32_t kCsV8 = kCsK + kCsKStages * kCsTile8;  // 2 V tiles of codes
+constexpr uint32_t kCsVf = kCsV8 + 2 * kCsTile8;          // 2 fp16 V tiles (second use: O staging)
+constexpr uint32_t kCsBar = kCsVf + 2 * kTileBytes;       // 48 barrier slots; the last holds the TMEM address
+constexpr uint32_t kCsRec = kCsBar + 384;                 // tile records
+constexpr int kCsBatch = 8, kCsBatches = 3;
+
+struct CsTile {
+    int32_t row[4];     // pool row of each 32-key quarter
+    float ks[4], lv[4], iv[4];  // scale of K, log2 and reciprocal of V's
+    uint32_t kv4;       // keys that exist in each quarter, 8 bits each
+    int32_t qrow;       // first row of the query block in [H * Np]
+    int32_t first, last;  // of its item; last < 0: past the end of this CTA's work
+};
+static_assert(sizeof(CsTile) == 80, "tile record");
+
+constexpr uint32_t kCsFac = kCsRec + kCsBatch * kCsBatches * sizeof(CsTile);  // [4][128] reciprocal row factors
+constexpr uint32_t kCsXsum = kCsFac + 4 * 128 * 4;                            // [2 groups][128 rows] partial sums
+constexpr uint32_t kCsSmem = kCsXsum + 2 * 128 * 4;
+static_assert(kCsSmem <= 232448, "shared memory");
+
+enum : uint32_t {
+    C_Q_FULL0 = 0, C_Q_EMPTY0 = 2, C_K_FULL0 = 4, C_K_EMPTY0 = 7, C_V8_FULL0 = 10, C_V8_EMPTY0 = 12, C_VF_FULL0 = 14,
+    C_S_FULL0 = 16, C_P_FULL0 = 18, C_PV_DONE0 = 20, C_STAGED0 = 22, C_FLUSHED0 = 24, C_REC_FULL0 = 26,
+    C_REC_EMPTY0 = 29, C_SUM_X = 32, C_O_FREE, C_MMA_DONE, C_COUNT
+};
+
+struct CacheSparseArgs {
+    CacheGeom g;
+    const float* k_scale;
+    const float* v_scale;
+    const __nv_bfloat16* q;
+    float* lse;               // may be null
+    int heads, group;         // query heads of one sequence; query heads that share a kv head
+    int Np, nq, n_items;
+    int sub;                  // blocks of a 128-key tile
+    float scale_log2;
+    const int32_t* indptr;    // null: every block of the sequence
+    const int32_t* kv_idx;
+    const int32_t* order;     // null: ascending
+    unsigned long long wait_limit_ns;
+};
+
+__device__ __forceinline__ void tc_mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor with A and B of format 0 (fp16 for kind::f16, e4m3 for kind::f8f6f4) and fp32 D.
+__host__ __device__ constexpr uint32_t idesc_fmt0_f32(int M, int N, bool b_mn_major) {
+    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+constexpr float kCsBias = 7.0f;   // weights are kept at 2^7 of their size: at most 2^15 when the reference lags by 2^8
+
+__global__ void __launch_bounds__(kCsThreads, 1)
+    cache_sparse_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CacheSparseArgs a) {
+    extern __shared__ __align__(1024) uint8_t cs_smem[];
+    const uint32_t base = smem_addr(cs_smem);
+    if (base & 1023u) {
+        if (threadIdx.x == 0) atomicOr(&g_device_error, kDevErrBadData);
+        return;
+    }
+    auto BAR = [&](uint32_t s) { return base + kCsBar + 8u * s; };
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(cs_smem + kCsBar + 47 * 8);
+    CsTile* const recs = reinterpret_cast<CsTile*>(cs_smem + kCsRec);
+    float* const fac = reinterpret_cast<float*>(cs_smem + kCsFac);
+    float* const xsum = reinterpret_cast<float*>(cs_smem + kCsXsum);
+
+    const int warp = threadIdx.x >> 5;
+    const uint32_t lane = lane_id();
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < C_COUNT; ++s) {
+            uint32_t cnt = 1;
+            if (s == C_P_FULL0 || s == C_P_FULL0 + 1 || s == C_STAGED0 || s == C_STAGED0 + 1 || s == C_SUM_X ||
+                s == C_O_FREE)
+                cnt = 256;  // softmax threads
+            else if (s == C_Q_FULL0 || s == C_Q_FULL0 + 1 || (s >= C_V8_EMPTY0 && s < C_V8_EMPTY0 + 2) ||
+                     (s >= C_VF_FULL0 && s < C_VF_FULL0 + 2))
+                cnt = 128;  // warps 12..15
+            else if (s >= C_REC_EMPTY0 && s < C_REC_EMPTY0 + kCsBatches)
+                cnt = 15;   // every warp but the reader
+            mbar_init(BAR(s), cnt);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+        tma_prefetch_desc(&tmO);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    const uint32_t tS = tmem, tO = tmem + 256u, tP = tmem + 384u;
+    const unsigned long long lim = a.wait_limit_ns;
+
+    // Record of tile n (null on a timeout); every lane of a warp calls it for every tile, in order. A warp gives a batch
+    // back after its last tile.
+    auto record = [&](uint32_t n) -> const CsTile* {
+        const uint32_t k = n / kCsBatch, sl = k % kCsBatches;
+        if (n % kCsBatch == 0 && !wait_bounded_warp(BAR(C_REC_FULL0 + sl), (k / kCsBatches) & 1u, lim)) return nullptr;
+        return &recs[sl * kCsBatch + n % kCsBatch];
+    };
+    auto release = [&](uint32_t n) {
+        if (n % kCsBatch == kCsBatch - 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C_REC_EMPTY0 + (n / kCsBatch) % kCsBatches));
+        }
+    };
+
+    // Registers: 128 x 56 + 256 x 176 + 128 x 104 is what 512 x 128 were launched with.
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+        if (warp == 3) {
+            // ------------------------------------------------------------------------------------------ reader
+            uint32_t bad = 0;
+            int r = 0;                       // next round
+            int w_id = -1, w_begin = 0, w_count = 0;  // this lane's item of the current window of 32 rounds
+            int id = 0, begin = 0, count = 0, tiles = 0, t = 0;  // the current item
+            bool ended = false;
+            for (uint32_t k = 0; !ended; ++k) {
+                const uint32_t sl = k % kCsBatches;
+                if (!wait_bounded_warp(BAR(C_REC_EMPTY0 + sl), ((k / kCsBatches) & 1u) ^ 1u, lim)) break;
+                int m_id = 0, m_begin = 0, m_count = 0, m_t = 0, m_first = 0, m_last = -1;  // tile `lane` of the batch
+                for (int i = 0; i < kCsBatch && !ended; ++i) {
+                    while (t == tiles && !ended) {  // next item
+                        if ((r & 31) == 0) {
+                            const int rr = r + (int)lane, G = gridDim.x, b = blockIdx.x;
+                            const int64_t w = (int64_t)rr * G + ((rr & 1) ? (G - 1 - b) : b);
+                            w_id = -1;
+                            w_count = 0;
+                            if (w < a.n_items) {
+                                w_id = a.order ? a.order[w] : (int)w;
+                                if (w_id < 0 || w_id >= a.n_items) {
+                                    bad = 1;
+                                    w_id = -2;  // not an item: skipped
+                                } else if (a.indptr) {
+                                    w_begin = a.indptr[w_id];
+                                    w_count = a.indptr[w_id + 1] - w_begin;
+                                    if (w_count < 0 || w_begin < 0) {
+                                        bad = 1;
+                                        w_count = 0;
+                                    }
+                                } else {
+                                    const int64_t len = a.g.lens[w_id / a.nq / a.heads];
+                                    w_begin = 0;
+                                    w_count = (int)min((int64_t)a.g.table_stride,
+                                                       max(len, (int64_t)0) / a.g.page + (max(len, (int64_t)0) % a.g.page != 0));
+                                }
+                            }
+                        }
+                        id = __shfl_sync(0xffffffffu, w_id, r & 31);
+                        begin = __shfl_sync(0xffffffffu, w_begin, r & 31);
+                        count = __shfl_sync(0xffffffffu, w_count, r & 31);
+                        ++r;
+                        t = 0;
+                        tiles = id == -2 ? 0 : max(1, (count + a.sub - 1) / a.sub);  // an empty list still writes its rows
+                        if (id == -1) ended = true;
+                    }
+                    if ((int)lane == i && !ended) {
+                        m_id = id;
+                        m_begin = begin;
+                        m_count = count;
+                        m_t = t;
+                        m_first = t == 0;
+                        m_last = t == tiles - 1;
+                    }
+                    ++t;
+                }
+                const int src = (int)lane >> 2, g = (int)lane & 3;
+                const int q_id = __shfl_sync(0xffffffffu, m_id, src), q_begin = __shfl_sync(0xffffffffu, m_begin, src);
+                const int q_count = __shfl_sync(0xffffffffu, m_count, src), q_t = __shfl_sync(0xffffffffu, m_t, src);
+                const int q_first = __shfl_sync(0xffffffffu, m_first, src), q_last = __shfl_sync(0xffffffffu, m_last, src);
+                const int h = q_id / a.nq, seq = h / a.heads, kvh = (h - seq * a.heads) / a.group;
+                int valid = 0, row = 0;
+                float ks = 1.0f, vs = 1.0f;
+                const int e = q_t * a.sub + ((g * a.sub) >> 2);
+                if (q_last >= 0 && e < q_count) {
+                    const int off = (g & (4 / a.sub - 1)) * 32;
+                    const int j = a.indptr ? a.kv_idx[q_begin + e] : e;
+                    int64_t len = a.g.lens[seq];
+                    if (len < 0 || len > (int64_t)a.g.table_stride * a.g.page) {
+                        bad = 1;
+                        len = len < 0 ? 0 : (int64_t)a.g.table_stride * a.g.page;
+                    }
+                    if (j < 0 || j >= a.g.table_stride) {
+                        bad = 1;
+                    } else {
+                        valid = (int)min((int64_t)32, max((int64_t)0, len - ((int64_t)j * a.g.page + off)));
+                        if (valid > 0) {
+                            const int page = a.g.table[(int64_t)seq * a.g.table_stride + j];
+                            if (page < 0 || page >= a.g.n_pages) {
+                                bad = 1;
+                                valid = 0;
+                            } else {
+                                const int64_t ph = (int64_t)page * a.g.kv_heads + kvh;
+                                row = (int)(ph * a.g.page) + off;
+                                ks = a.k_scale[ph];
+                                vs = fmaxf(a.v_scale[ph], 1e-30f);
+                            }
+                        }
+                    }
+                }
+                CsTile* const rec = &recs[sl * kCsBatch + src];
+                rec->row[g] = row;
+                rec->ks[g] = ks;
+                rec->lv[g] = __log2f(vs);
+                rec->iv[g] = 1.0f / vs;
+                reinterpret_cast<uint8_t*>(&rec->kv4)[g] = (uint8_t)valid;
+                if (g == 0) {
+                    rec->qrow = h * a.Np + (q_id - h * a.nq) * kTcRows;
+                    rec->first = q_first;
+                    rec->last = q_last;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(C_REC_FULL0 + sl));
+            }
+            if (bad) atomicOr(&g_device_error, kDevErrBadData);
+        } else if (warp == 0 || warp == 2) {
+            // ------------------------------------------------------------------------- TMA: K codes, V codes
+            const bool keys = warp == 0;
+            const uint64_t pol = l2_policy_evict_last();
+            const uint32_t stages = keys ? kCsKStages : 2u;
+            const uint32_t full = keys ? C_K_FULL0 : C_V8_FULL0, empty = keys ? C_K_EMPTY0 : C_V8_EMPTY0;
+            const uint32_t ring = base + (keys ? kCsK : kCsV8);
+            uint32_t n = 0, filled = 0;
+            for (;; ++n) {
+                const CsTile* const rec = record(n);
+                if (!rec || rec->last < 0) break;
+                const uint32_t s = n % stages;
+                if (!wait_bounded_warp(BAR(empty + s), ((n / stages) & 1u) ^ 1u, lim)) break;
+                if (lane == 0) mbar_arrive_expect_tx(BAR(full + s), kCsTile8);
+                __syncwarp();
+                if (lane < 4)
+                    tma_load_2d_hint(ring + s * kCsTile8 + lane * 4096u, keys ? &tmK : &tmV, 0, rec->row[lane],
+                                     BAR(full + s), pol);
+                filled = n + 1;
+                release(n);
+            }
+            for (uint32_t i = 1; i <= stages && i <= filled; ++i) {  // copies in flight land before the CTA ends
+                const uint32_t x = filled - i;
+                wait_bounded(BAR(full + x % stages), (x / stages) & 1u, kDrainLimitNs);
+            }
+            __syncwarp();
+        } else {
+            // ---------------------------------------------------------------------------------- MMA issuer
+            constexpr uint32_t kIdQK = idesc_fmt0_f32(128, 128, false);
+            constexpr uint32_t kIdPV = idesc_fmt0_f32(128, 128, true);
+            const uint64_t dQ0 = smem_desc(base + kCsQ, 16, 1024), dK0 = smem_desc(base + kCsK, 16, 1024);
+            const uint64_t dV0 = smem_desc(base + kCsVf, kBoxBytes, 1024);
+            uint32_t n = 0, items = 0;  // items whose first tile has been issued
+            bool pend = false, pend_first = false;
+            uint32_t pend_n = 0, pend_item = 0;
+            auto issue_pv = [&]() -> bool {
+                const uint32_t b = pend_n & 1u, par = (pend_n >> 1) & 1u;
+                if (!wait_bounded_warp(BAR(C_P_FULL0 + b), par, lim)) return false;
+                if (!wait_bounded_warp(BAR(C_VF_FULL0 + b), par, lim)) return false;
+                if (pend_first && pend_item > 0 && !wait_bounded_warp(BAR(C_O_FREE), (pend_item - 1) & 1u, lim))
+                    return false;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t dV = dV0 + b * (kTileBytes >> 4);
+#pragma unroll
+                    for (uint32_t kk = 0; kk < 8; ++kk)
+                        tc_mma_ts(tO, tP + b * 64u + kk * 8u, dV + kk * 128u, kIdPV, (pend_first && kk == 0) ? 0u : 1u);
+                    tc_commit(BAR(C_PV_DONE0 + b));
+                }
+                __syncwarp();
+                pend = false;
+                return true;
+            };
+            bool ok = true;
+            for (;; ++n) {
+                const CsTile* const rec = record(n);
+                if (!rec) {
+                    ok = false;
+                    break;
+                }
+                const int first = rec->first, last = rec->last;
+                if (last < 0) break;
+                release(n);
+                if (first) {
+                    ++items;
+                    if (!(ok = wait_bounded_warp(BAR(C_Q_FULL0 + ((items - 1) & 1u)), ((items - 1) >> 1) & 1u, lim)))
+                        break;
+                }
+                const uint32_t qs = (items - 1) & 1u, ks = n % kCsKStages, b = n & 1u;
+                if (!(ok = wait_bounded_warp(BAR(C_K_FULL0 + ks), (n / kCsKStages) & 1u, lim))) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t dQ = dQ0 + qs * (2 * kCsTile8 >> 4), dK = dK0 + ks * (kCsTile8 >> 4);
+#pragma unroll
+                    for (uint32_t kk = 0; kk < 8; ++kk)  // four steps of q1, four of q2, over the same K
+                        tc_mma_ss_f8(tS + b * 128u, dQ + (kk >> 2) * (kCsTile8 >> 4) + (kk & 3u) * 2u,
+                                     dK + (kk & 3u) * 2u, kIdQK, kk ? 1u : 0u);
+                    tc_commit(BAR(C_S_FULL0 + b));
+                    tc_commit(BAR(C_K_EMPTY0 + ks));
+                    if (last) tc_commit(BAR(C_Q_EMPTY0 + qs));
+                }
+                __syncwarp();
+                if (pend && !(ok = issue_pv())) break;
+                pend = true;
+                pend_first = first;
+                pend_n = n;
+                pend_item = items - 1;
+            }
+            if (ok && pend) issue_pv();
+            if (lane == 0) {
+                tc_commit(BAR(C_MMA_DONE));
+                wait_bounded(BAR(C_MMA_DONE), 0, kDrainLimitNs);
+            }
+            __syncwarp();
+        }
+    } else if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;" ::: "memory");
+        // ------------------------------------------------------------------- Q split, V widening, O stores
+        const int wt = warp - 12;
+        bool fin[2] = {false, false};
+        int32_t fin_row[2] = {0, 0};
+        uint32_t staged[2] = {0, 0}, flushed[2] = {0, 0};
+        uint32_t items = 0;
+        bool ok = true;
+        // Q rows of the block as q1 + q2, swizzled like a TMA tile; 16 lanes of a warp hold a row.
+        auto split_q = [&](int32_t qrow) -> bool {
+            const uint32_t qs = items & 1u;
+            if (!wait_bounded_warp(BAR(C_Q_EMPTY0 + qs), ((items >> 1) & 1u) ^ 1u, lim)) return false;
+            const uint32_t dst = base + kCsQ + qs * 2 * kCsTile8;
+            const uint32_t col = lane & 15u;
+            const __nv_bfloat16* const src = a.q + (size_t)qrow * kTcDim + col * 8;
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                uint4 w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = (part * 8 + i) * 8 + wt * 2 + (int)(lane >> 4);
+                    w[i] = __ldcs(reinterpret_cast<const uint4*>(src + (size_t)row * kTcDim));
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = (part * 8 + i) * 8 + wt * 2 + (int)(lane >> 4);
+                    float f[8];
+                    RopeVec<__nv_bfloat16>::unpack(w[i], f);
+                    uint32_t amax = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t u = __float_as_uint(f[e]) & 0x7fffffffu;
+                        amax = max(amax, u < 0x7f800000u ? u : 0u);
+                    }
+#pragma unroll
+                    for (int x = 8; x; x >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, x));
+                    const float s = row_factor(amax);
+                    uint32_t c1[2], c2[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        c1[x] = c2[x] = 0;
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float u0 = f[4 * x + 2 * y] * s, u1 = f[4 * x + 2 * y + 1] * s;
+                            const uint32_t q1 = e4m3x2(u0, u1);
+                            const uint32_t hh = half2_of_e4m3x2(q1);
+                            const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&hh));
+                            c1[x] |= q1 << (16 * y);
+                            c2[x] |= e4m3x2(u0 - z.x, u1 - z.y) << (16 * y);
+                        }
+                    }
+                    const uint32_t at = dst + row * 128u + ((((col >> 1) ^ ((uint32_t)row & 7u)) << 4) | (8u * (col & 1u)));
+                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(c1[0]), "r"(c1[1]) : "memory");
+                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + kCsTile8), "r"(c2[0]), "r"(c2[1])
+                                 : "memory");
+                    // four items deep: the slot of item k is written again for item k + 4, whose split follows P V of item
+                    // k, while Q's two slots only follow Q K^T, which the softmax may not have read yet
+                    if (col == 0) fac[(items & 3u) * 128 + row] = 1.0f / s;
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(BAR(C_Q_FULL0 + qs));
+            ++items;
+            return true;
+        };
+        // The O staged in slot sl leaves for global memory; returns once the slot has been read.
+        auto flush = [&](uint32_t sl) -> bool {
+            if (!wait_bounded_warp(BAR(C_STAGED0 + sl), staged[sl] & 1u, lim)) return false;
+            ++staged[sl];
+            if (warp == 12 && lane == 0) {
+                tma_store_2d(&tmO, base + kCsVf + sl * kTileBytes, 0, fin_row[sl]);
+                tma_store_2d(&tmO, base + kCsVf + sl * kTileBytes + kBoxBytes, 64, fin_row[sl]);
+                bulk_commit_group();
+                bulk_wait_read_all();
+                mbar_arrive(BAR(C_FLUSHED0 + sl));
+            }
+            __syncwarp();
+            if (!wait_bounded_warp(BAR(C_FLUSHED0 + sl), flushed[sl] & 1u, lim)) return false;
+            ++flushed[sl];
+            fin[sl] = false;
+            return true;
+        };
+        uint32_t n = 0;
+        const CsTile* rec = record(0);
+        ok = rec != nullptr;
+        if (ok && rec->last >= 0) ok = split_q(rec->qrow);
+        while (ok && rec->last >= 0) {
+            const uint32_t kv4 = rec->kv4;
+            const int last = rec->last;
+            const int32_t qrow = rec->qrow;
+            const CsTile* const next = record(n + 1);
+            if (!(ok = next != nullptr)) break;
+            if (next->last >= 0 && next->first && !(ok = split_q(next->qrow))) break;
+            const uint32_t b = n & 1u, par = (n >> 1) & 1u;
+            if (n >= 2) {
+                if (fin[b]) ok = flush(b);
+                else ok = wait_bounded_warp(BAR(C_PV_DONE0 + b), ((n - 2) >> 1) & 1u, lim);
+                if (!ok) break;
+            }
+            if (!(ok = wait_bounded_warp(BAR(C_V8_FULL0 + b), par, lim))) break;
+            const uint32_t src = base + kCsV8 + b * kCsTile8, dst = base + kCsVf + b * kTileBytes;
+            const uint32_t c16 = lane & 7u;  // 16 dimensions of a key row
+            // the two halves of the row's columns write their 16-byte pieces in opposite order: no bank conflicts
+            const uint32_t flip = c16 >> 2;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t row = (uint32_t)(i * 16 + wt * 4) + (lane >> 3);
+                uint4 w = ld_shared_v4(src + row * 128u + (c16 << 4));
+                if ((row & 31u) >= ((kv4 >> (8 * (i >> 1))) & 255u)) w = make_uint4(0, 0, 0, 0);
+                const uint32_t at = dst + (c16 >> 2) * kBoxBytes + row * 128u;
+                const uint32_t j = 2u * (c16 & 3u);
+                const uint32_t lo0 = flip ? w.z : w.x, lo1 = flip ? w.w : w.y, hi0 = flip ? w.x : w.z, hi1 = flip ? w.y : w.w;
+                st_shared_v4(at + (((j + flip) ^ (row & 7u)) << 4), half2_of_e4m3x2(lo0 & 0xffffu),
+                             half2_of_e4m3x2(lo0 >> 16), half2_of_e4m3x2(lo1 & 0xffffu), half2_of_e4m3x2(lo1 >> 16));
+                st_shared_v4(at + (((j + 1u - flip) ^ (row & 7u)) << 4), half2_of_e4m3x2(hi0 & 0xffffu),
+                             half2_of_e4m3x2(hi0 >> 16), half2_of_e4m3x2(hi1 & 0xffffu), half2_of_e4m3x2(hi1 >> 16));
+            }
+            mbar_arrive(BAR(C_V8_EMPTY0 + b));
+            fence_proxy_async_smem();
+            mbar_arrive(BAR(C_VF_FULL0 + b));
+            fin[b] = last;
+            fin_row[b] = qrow;
+            release(n);
+            rec = next;
+            ++n;
+        }
+        for (uint32_t x = 0; ok && x < 2; ++x) {  // the last items' O, oldest slot first
+            const uint32_t sl = (n + x) & 1u;
+            if (fin[sl]) ok = flush(sl);
+        }
+        if (warp == 12 && lane == 0) bulk_wait_all();
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;" ::: "memory");
+        // ----------------------------------------------------------------------------- softmax warpgroups
+        const uint32_t grp = (uint32_t)(warp - 4) >> 2;  // keys 64 grp .. 64 grp + 63 of every tile
+        const uint32_t wl = (uint32_t)warp & 3u;
+        const int row = (int)(wl * 32u + lane);
+        const uint32_t lane_off = (wl * 32u) << 16;
+        uint32_t n = 0, n_epi = 0, items = 0;
+        bool ok = true;
+        bool pend = false;  // an item's epilogue waits until the next item's first P is stored
+        size_t pd_grow = 0;
+        float pd_m = 0.0f, pd_l = 0.0f;
+        uint32_t pd_nl = 0;
+        auto epilogue = [&]() -> bool {
+            const uint32_t bl = pd_nl & 1u;
+            if (!wait_bounded_warp(BAR(C_PV_DONE0 + bl), (pd_nl >> 1) & 1u, lim)) return false;  // the item's last P V
+            xsum[grp * 128u + (uint32_t)row] = pd_l;
+            mbar_arrive(BAR(C_SUM_X));
+            if (!wait_bounded_warp(BAR(C_SUM_X), n_epi & 1u, lim)) return false;
+            const float l_all = pd_l + xsum[(grp ^ 1u) * 128u + (uint32_t)row];
+            const float inv_l = l_all == 0.0f ? 0.0f : 1.0f / l_all;  // a row that saw no key gives zeros
+            tc_fence_after();
+            uint32_t ov[2][32];
+            tmem_ld32(tO + grp * 64u + lane_off, ov[0]);
+            tmem_ld32(tO + grp * 64u + lane_off + 32u, ov[1]);
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive(BAR(C_O_FREE));
+            const uint32_t stage = base + kCsVf + bl * kTileBytes + grp * kBoxBytes;
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    const uint32_t j = (uint32_t)(ch * 4 + q4);
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k2 = 0; k2 < 4; ++k2)
+                        w[k2] = pack_bf16x2(__uint_as_float(ov[ch][q4 * 8 + 2 * k2]) * inv_l,
+                                            __uint_as_float(ov[ch][q4 * 8 + 2 * k2 + 1]) * inv_l);
+                    st_shared_v4(stage + (uint32_t)row * 128u + ((j ^ ((uint32_t)row & 7u)) << 4), w[0], w[1], w[2],
+                                 w[3]);
+                }
+            fence_proxy_async_smem();
+            mbar_arrive(BAR(C_STAGED0 + bl));
+            if (a.lse && grp == 0)
+                a.lse[pd_grow] = l_all == 0.0f ? -INFINITY : (pd_m - kCsBias + lg2_approx(l_all)) * 0.6931471805599453f;
+            ++n_epi;
+            return true;
+        };
+        float c = 0.0f, m = -INFINITY, l_run = 0.0f;
+        for (;; ++n) {
+            const CsTile* const rec = record(n);
+            if (!(ok = rec != nullptr) || rec->last < 0) break;
+            const int first = rec->first, last = rec->last;
+            const uint32_t kv4 = rec->kv4, b = n & 1u;
+            const int32_t qrow = rec->qrow;
+            const uint32_t q0 = 2u * grp, o0 = 2u - q0;  // this group's quarters, the other group's
+            float ks[2] = {rec->ks[q0], rec->ks[q0 + 1]}, lv[2] = {rec->lv[q0], rec->lv[q0 + 1]};
+            const float iv[2] = {rec->iv[q0], rec->iv[q0 + 1]};
+            float oks[2] = {rec->ks[o0], rec->ks[o0 + 1]}, olv[2] = {rec->lv[o0], rec->lv[o0 + 1]};
+            release(n);
+            const uint32_t tSb = tS + b * 128u;
+            if (!(ok = wait_bounded_warp(BAR(C_S_FULL0 + b), (n >> 1) & 1u, lim))) break;
+            tc_fence_after();
+            if (first) {  // the row factors were written before Q K^T could start
+                c = fmaxf(a.scale_log2 * fac[(items & 3u) * 128u + (uint32_t)row], 1e-37f);
+                m = -INFINITY;
+                l_run = 0.0f;
+                ++items;
+            }
+            // Row maximum of x over the whole tile, without an exchange between the groups: per 32-key quarter the largest
+            // S, then the quarter's scales.
+            auto quarter_max = [&](const float* s, uint32_t have) -> float {
+                float mx[4];
+                if (have == 32u) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[e] = fmax3(s[e], s[4 + e], s[8 + e]);
+#pragma unroll
+                    for (int x = 12; x < 28; x += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mx[e] = fmax3(mx[e], s[x + e], s[x + 4 + e]);
+                    return fmaxf(fmax3(mx[0], mx[1], fmaxf(s[28], s[29])), fmax3(mx[2], mx[3], fmaxf(s[30], s[31])));
+                }
+                float r = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) r = (uint32_t)e < have ? fmaxf(r, s[e]) : r;
+                return r;
+            };
+            float top;
+            {
+                float o[64];
+                tmem_ld32(tSb + (grp ^ 1u) * 64u + lane_off, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+                tmem_ld32(tSb + (grp ^ 1u) * 64u + lane_off + 32u, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+                tmem_wait_ld();
+                const float m0 = quarter_max(o, (kv4 >> (8 * o0)) & 255u);
+                const float m1 = quarter_max(o + 32, (kv4 >> (8 * o0 + 8)) & 255u);
+                top = fmaxf(fmaf(m0, oks[0] * c, olv[0]), fmaf(m1, oks[1] * c, olv[1]));
+            }
+            float s[64];
+            tmem_ld32(tSb + grp * 64u + lane_off, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            tmem_ld32(tSb + grp * 64u + lane_off + 32u, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+            tmem_wait_ld();
+            const uint32_t k0 = (kv4 >> (8 * q0)) & 255u, k1 = (kv4 >> (8 * q0 + 8)) & 255u;
+            {
+                const float m0 = quarter_max(s, k0), m1 = quarter_max(s + 32, k1);
+                top = fmaxf(top, fmaxf(fmaf(m0, ks[0] * c, lv[0]), fmaf(m1, ks[1] * c, lv[1])));
+            }
+            // The reference moves when a row sees its first key, or when the maximum exceeds it by more than 2^8.
+            float alpha = 1.0f;
+            if (m == -INFINITY) {
+                m = top;
+            } else if (top - m > 8.0f) {
+                alpha = ex2_approx(m - top);
+                m = top;
+            }
+            const float ref = m == -INFINITY ? 0.0f : kCsBias - m;
+            uint32_t pw[32];
+            float sum[2];
+#pragma unroll
+            for (int qd = 0; qd < 2; ++qd) {
+                const float ck = ks[qd] * c, off = lv[qd] + ref;
+                const uint32_t have = qd ? k1 : k0;
+                float la, lb, lc, ld;
+                uint64_t l2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+                if (have == 32u) {
+                    const uint64_t c2 = f2_pack(ck, ck), o2 = f2_pack(off, off);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const uint64_t xx = f2_fma(f2_pack(s[32 * qd + 2 * e], s[32 * qd + 2 * e + 1]), c2, o2);
+                        float x0, x1;
+                        f2_unpack(xx, x0, x1);
+                        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                        pw[16 * qd + e] = pack_f16x2(p0, p1);
+                        l2[e & 1] = f2_add(l2[e & 1], f2_pack(p0, p1));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float p0 = 2u * e < have ? ex2_approx(fmaf(s[32 * qd + 2 * e], ck, off)) : 0.0f;
+                        const float p1 = 2u * e + 1u < have ? ex2_approx(fmaf(s[32 * qd + 2 * e + 1], ck, off)) : 0.0f;
+                        pw[16 * qd + e] = pack_f16x2(p0, p1);
+                        l2[e & 1] = f2_add(l2[e & 1], f2_pack(p0, p1));
+                    }
+                }
+                f2_unpack(l2[0], la, lb);
+                f2_unpack(l2[1], lc, ld);
+                sum[qd] = (la + lb) + (lc + ld);
+            }
+            l_run = fmaf(l_run, alpha, fmaf(sum[0], iv[0], sum[1] * iv[1]));
+            // this group rescales its 64 columns of O once P V of tile n - 1 has added to them
+            if (!first && __any_sync(0xffffffffu, alpha != 1.0f)) {
+                if (!(ok = wait_bounded_warp(BAR(C_PV_DONE0 + (b ^ 1u)), ((n - 1) >> 1) & 1u, lim))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch) {
+                    uint32_t ov[32];
+                    tmem_ld32(tO + grp * 64u + lane_off + ch * 32u, ov);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                    tmem_st32(tO + grp * 64u + lane_off + ch * 32u, ov);
+                }
+            }
+            tmem_st32(tP + b * 64u + grp * 32u + lane_off, pw);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(BAR(C_P_FULL0 + b));
+            if (first && pend) {
+                if (!(ok = epilogue())) break;
+                pend = false;
+            }
+            if (last) {
+                pend = true;
+                pd_grow = (size_t)qrow + row;
+                pd_m = m;
+                pd_l = l_run;
+                pd_nl = n;
+            }
+        }
+        if (ok && pend) epilogue();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace losa

@@ -25,6 +25,7 @@ constexpr unsigned int kDevErrBadData = 2u;
 #include "attn_sparse.cuh"
 #include "cache_append.cuh"
 #include "cache_attn.cuh"
+#include "cache_sparse.cuh"
 #include "ptx.cuh"
 #include "rope.cuh"
 #include "select.cuh"

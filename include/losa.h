@@ -288,6 +288,28 @@ losa_status losa_cache_attn(const losa_cache* cache, int32_t heads, int32_t toke
                             int64_t o_seq_stride, int64_t o_token_stride, int64_t o_head_stride, float* lse,
                             void* workspace, size_t ws_bytes, cudaStream_t stream);
 
+/*
+ * Block-sparse (or dense) attention over the cache: losa_sparse_attn with its keys and values in the paged 8-bit cache.
+ *   shape     : query side, bf16, head_dim 128, block_q 128, block_k = the cache's page_tokens (128, 64 or 32). heads is
+ *               seqs * H, sequence-major; query head h of a sequence reads kv head h / (H / kv_heads).
+ *   q, o      : [heads][Np][128]; lse: [heads][Np] fp32 or NULL. o must not overlap q.
+ *   indptr, kv_block_idx : CSR lists of blocks of the sequence per (head, query block), in any order, as for
+ *               losa_sparse_attn; both NULL: every block the sequence holds. An entry in [0, table_stride) behind the
+ *               sequence's last token adds no keys (a frozen pattern may run ahead of the cache). kv_block_idx must hold
+ *               indptr's last entry: the library cannot check that.
+ *   order     : work order, or NULL, as for losa_sparse_attn.
+ *   scale     : logit scale, > 0.
+ * A row that sees no key (an empty list, an empty sequence) gets o = 0 and lse = -inf. Query elements below 2^-9 of their
+ * row's largest are off by at most 2^-17 of it; weights are rounded to fp16 for the product with V; the rest is fp32. Codes of
+ * slots that hold no token are never used. A block, page, length, offset or work-order entry out of range sets the device
+ * error word (LOSA_ERR_DEVICE_FAULT); the blocks concerned are left out.
+ */
+losa_status losa_cache_sparse_attn(const losa_shape* shape, const losa_cache* cache, const void* q,
+                                   const int32_t* page_table, const int32_t* lens, const void* k8, const void* v8,
+                                   const float* k_scale, const float* v_scale, float scale, const int32_t* indptr,
+                                   const int32_t* kv_block_idx, const int32_t* order, void* o, float* lse,
+                                   cudaStream_t stream);
+
 /* Scratch bytes losa_cache_attn needs on the current device (0 where the keys are not split, or for bad arguments). */
 size_t losa_cache_attn_workspace_bytes(const losa_cache* cache, int32_t heads, int32_t tokens, int32_t max_len);
 

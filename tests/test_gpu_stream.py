@@ -6,7 +6,8 @@ Tolerances. A value rounded once to type t is off by at most eps(t) / 2 of it: 2
     6 * 2^-24 of |a| + |b|, then the rounding to the type;
   * codes: a value within 1e-5 of a rounding border (relative) may fall on either side; every other code is exact;
   * attention: weights rounded to fp16 (2^-11 each, either side of the quotient) and the output rounded to bf16:
-    |dO| <= 2^-8 |O| + 2^-10 sum_j p_j |v_j|; lse: fp32 sums of products, 1e-4."""
+    |dO| <= 2^-8 |O| + 2^-10 sum_j p_j |v_j|; lse: fp32 sums of products, 1e-4, and for large logits what a sum of 256
+    fp32 products (two terms for each of 128 dimensions) can be off by, 256 * 2^-24 |lse|."""
 import math
 
 import pytest
@@ -307,7 +308,7 @@ def attn_close(o, lse, want, want_lse, size):
     assert bool((err <= bound).all()), float((err / bound).max())
     empty = want_lse == -math.inf
     assert torch.equal(empty, lse.double() == -math.inf)
-    assert bool(((lse.double() - want_lse)[~empty].abs() <= 1e-4).all())
+    assert bool(((lse.double() - want_lse).abs() <= 1e-4 + 256 * 2.0 ** -24 * want_lse.abs())[~empty].all())
 
 
 def poisoned_cache(g, lens, hk, page, d, width, spread=4):
@@ -428,3 +429,137 @@ def test_cache_attn_bad_pages_and_lengths_are_reported():
     L.losa_cache_attn(cache, q, k8, v8, ks, vs, table, torch.tensor([-3, 65], dtype=torch.int32, device="cuda"), 0.1, o)
     assert L.losa_get_device_error() == -5
     assert not o[0].any()
+
+
+# ------------------------------------------------------------------------------------------------------ blocked queries
+
+def random_lists(g, items, width, lo, hi, empty_every=0):
+    counts = torch.randint(lo, hi + 1, (items,), generator=g, device="cuda")
+    if empty_every:
+        counts[::empty_every] = 0
+    order_of = torch.rand(items, width, generator=g, device="cuda").argsort(1)  # distinct blocks, in any order
+    keep = torch.arange(width, device="cuda")[None] < counts[:, None]
+    indptr = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).int()
+    return indptr, order_of[keep].int().contiguous()
+
+
+def check_blocks(q, o, lse, pool, table, lens, page, heads, hk, n, scale, indptr, blocks, items=None):
+    k8, v8, ks, vs = pool
+    nq = q.shape[1] // 128
+    H = q.shape[0]
+    per = heads // hk
+    ptr = None if indptr is None else indptr.tolist()
+    cached = {}
+    for item in (range(H * nq) if items is None else items):
+        h, i = divmod(item, nq)
+        b, kvh = h // heads, (h % heads) // per
+        if (b, kvh) not in cached:
+            cached = {(b, kvh): (dense(k8, ks, table, b, kvh, lens[b]), dense(v8, vs, table, b, kvh, lens[b]))}
+        k, v = cached[(b, kvh)]
+        if ptr is None:
+            key = torch.arange(lens[b], device="cuda")
+        else:
+            at = blocks[ptr[item]:ptr[item + 1]].long()
+            key = (at[:, None] * page + torch.arange(page, device="cuda")).flatten()
+            key = key[key < lens[b]]
+        rows = slice(i * 128, min(n, i * 128 + 128))
+        want, wl, size = attend(q[h, rows].double(), k[key], v[key],
+                                torch.full((q[h, rows].shape[0],), len(key), device="cuda"), scale)
+        attn_close(o[h, rows], lse[h, rows], want, wl, size)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page,lens,heads,hk,n,lo,hi,empty,ordered", [
+    (128, [1000], 1, 1, 100, 1, 1, 0, False),
+    (128, [129], 2, 1, 130, 1, 2, 0, True),
+    (32, [777], 2, 2, 300, 1, 9, 4, True),
+    (64, [640, 33], 4, 2, 257, 1, 5, 3, False),
+    (128, [0, 4000], 6, 2, 900, 1, 20, 5, True),
+    (32, [3000], 12, 12, 5000, 1, 3, 7, True),      # 480 items: several short items on every SM
+    (64, [1999], 3, 3, 128 * 99, 1, 12, 0, True),
+    (32, [20000], 2, 1, 4000, 100, 600, 0, True),   # long lists
+    (128, [513, 5, 2048], 2, 2, 385, 0, 0, 0, False),  # no lists: every block
+    (32, [100, 7000], 3, 1, 1, 0, 0, 0, False),
+])
+def test_cache_sparse_attn(page, lens, heads, hk, n, lo, hi, empty, ordered):
+    require_gpu()
+    g = gen(sum(lens) + n)
+    seqs = len(lens)
+    width = max(1, -(-max(lens) // page)) + 2  # lists may name blocks behind the sequence
+    k8, v8, ks, vs, table = poisoned_cache(g, lens, hk, page, 128, width)
+    H, nq = seqs * heads, -(-n // 128)
+    q = torch.randn(H, nq * 128, 128, generator=g, device="cuda").bfloat16()
+    q[0, 0] *= 2.0 ** 30  # a loud row, a quiet one and a zero one
+    q[0, 0] *= 2.0 ** -30
+    q[-1, 0] *= 2.0 ** -20
+    q[0, min(n - 1, 1)] = 0
+    q[:, n:] = math.nan  # padding rows hold anything
+    items = H * nq
+    indptr = blocks = order = None
+    if hi:
+        indptr, blocks = random_lists(g, items, width, lo, min(hi, width), empty)
+    if ordered:
+        order = torch.randperm(items, generator=g, device="cuda").int()
+    scale = 0.3 / math.sqrt(128)
+    o = torch.full_like(q, 9.0)
+    lse = torch.full((H, nq * 128), 9.0, device="cuda")
+    cache = L.make_cache(hk, 128, page, k8.shape[0], seqs, width)
+    L.losa_cache_sparse_attn(L.make_shape(H, n, nq * 128, 128, 128, page, "bf16"), cache, q, k8, v8, ks, vs, table,
+                             torch.tensor(lens, dtype=torch.int32, device="cuda"), scale, o, indptr=indptr,
+                             kv_block_idx=blocks, order=order, lse=lse)
+    assert L.losa_get_device_error() == 0
+    check_blocks(q, o, lse, (k8, v8, ks, vs), table, lens, page, heads, hk, n, scale, indptr, blocks)
+
+
+@pytest.mark.gpu
+def test_cache_sparse_attn_sinks_and_growing_rows():
+    """Rows whose maximum grows by far more than 2^8 from block to block, one key that outweighs 30000, loud and quiet
+    values: the reference moves, nothing overflows, and the tail under the sink is kept."""
+    require_gpu()
+    g = gen(11)
+    page, n = 128, 30000
+    width = -(-n // page)
+    k8, v8, ks, vs, table = poisoned_cache(g, [n], 1, page, 128, width, spread=6)
+    ks[table[0].long(), 0] = torch.exp2(-9 + torch.arange(width, device="cuda").float() / 40)
+    k8.view(torch.uint8)[int(table[0, 100]), 0, 7] = torch.full((128,), 448.0, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+    v8.view(torch.uint8)[int(table[0, 3])] = 0
+    vs[int(table[0, 3])] = 2.0 ** -40
+    q = torch.randn(1, 128, 128, generator=g, device="cuda").bfloat16()
+    q[0, :40] = 0.05
+    o, lse = torch.empty_like(q), torch.empty(1, 128, device="cuda")
+    cache = L.make_cache(1, 128, page, k8.shape[0], 1, width)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    for scale in (1.0, 0.05):
+        L.losa_cache_sparse_attn(L.make_shape(1, 128, 128, 128, 128, page, "bf16"), cache, q, k8, v8, ks, vs, table, lens,
+                                 scale, o, lse=lse)
+        assert L.losa_get_device_error() == 0
+        want, wl, size = attend(q[0].double(), dense(k8, ks, table, 0, 0, n), dense(v8, vs, table, 0, 0, n),
+                                torch.full((128,), n, device="cuda"), scale)
+        attn_close(o[0], lse[0], want, wl, size)
+
+
+@pytest.mark.gpu
+def test_cache_sparse_attn_reports_bad_input():
+    require_gpu()
+    g = gen(12)
+    page, n = 64, 256
+    k8, v8, ks, vs, table = poisoned_cache(g, [n], 1, page, 128, 4)
+    q = torch.randn(1, 256, 128, generator=g, device="cuda").bfloat16()
+    shape, cache = L.make_shape(1, 256, 256, 128, 128, page, "bf16"), L.make_cache(1, 128, page, k8.shape[0], 1, 4)
+    good = dict(table=table, lens=[n], indptr=[0, 2, 4], blocks=[0, 1, 2, 3], order=[0, 1])
+    i32 = lambda v: v if torch.is_tensor(v) else torch.tensor(v, dtype=torch.int32, device="cuda")
+    low = table.clone()
+    low[0, 1] = -1
+    for bad, left in ((dict(blocks=[0, 4, 2, 3]), [0]), (dict(blocks=[0, -1, 2, 3]), [0]), (dict(table=low), [0]),
+                      (dict(indptr=[0, 2, 1]), None), (dict(lens=[n + 1]), [0, 1]), (dict(order=[0, 2]), [0, 1])):
+        c = {**good, **bad}
+        o = torch.full_like(q, 9.0)
+        lse = torch.full((1, 256), 9.0, device="cuda")
+        L.losa_cache_sparse_attn(shape, cache, q, k8, v8, ks, vs, i32(c["table"]), i32(c["lens"]), 0.02, o,
+                                 indptr=i32(c["indptr"]), kv_block_idx=i32(c["blocks"]), order=i32(c["order"]), lse=lse)
+        assert L.losa_get_device_error() == -5, bad
+        if left is not None:  # item 0 over the blocks that are left
+            k, v = dense(k8, ks, table, 0, 0, n), dense(v8, vs, table, 0, 0, n)
+            key = torch.cat([torch.arange(j * page, j * page + page, device="cuda") for j in left])
+            want, wl, size = attend(q[0, :128].double(), k[key], v[key], torch.full((128,), len(key), device="cuda"), 0.02)
+            attn_close(o[0, :128], lse[0, :128], want, wl, size)
