@@ -80,8 +80,8 @@ CacheGeom cache_geom(const losa_cache* c, const int32_t* table, const int32_t* l
 }
 
 // Tensor map over the pool's codes as a [pages * kv heads * page tokens][d] byte matrix, boxes of box_rows whole rows,
-// swizzled over the row (64 or 128 bytes) or not.
-bool make_code_map(CUtensorMap* map, const losa_cache* c, const void* codes, uint32_t box_rows, bool swizzle = true) {
+// swizzled over the row (64 or 128 bytes).
+bool make_code_map(CUtensorMap* map, const losa_cache* c, const void* codes, uint32_t box_rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t gdim[2] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->n_pages * c->kv_heads * c->page_tokens};
@@ -90,8 +90,7 @@ bool make_code_map(CUtensorMap* map, const losa_cache* c, const void* codes, uin
     const cuuint32_t estride[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), gdim, gstride, box, estride,
               CU_TENSOR_MAP_INTERLEAVE_NONE,
-              !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
-                       : (c->head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B),
+              c->head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -371,7 +370,7 @@ losa_status losa_cache_sparse_attn(const losa_shape* shape, const losa_cache* ca
         !cache_supported(cache) || rows > 2147483647ll)
         return LOSA_ERR_UNSUPPORTED;
     CUtensorMap tk, tv, to;
-    if (!make_code_map(&tk, cache, k8, 32) || !make_code_map(&tv, cache, v8, 32, false) ||
+    if (!make_code_map(&tk, cache, k8, 32) || !make_code_map(&tv, cache, v8, 32) ||
         !make_tile_map(&to, o, (uint64_t)rows))
         return LOSA_ERR_CUDA;
     CacheSparseArgs a;

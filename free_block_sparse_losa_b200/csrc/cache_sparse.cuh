@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             const uint32_t dst = base + kCsQ + qs * 2 * kCsTile8;
             const uint32_t col = lane & 15u;
             const __nv_bfloat16* const src = a.q + (size_t)qrow * kTcDim + col * 8;
-#pragma unroll
+#pragma unroll 1
             for (int part = 0; part < 2; ++part) {
                 uint4 w[8];
 #pragma unroll
@@ -441,6 +441,8 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             fin[sl] = false;
             return true;
         };
+        const uint32_t c16 = (lane & 3u) | ((lane >> 3) & 1u) << 2;  // 16 dimensions of a key row
+        const uint32_t r0 = (lane >> 4) ^ ((lane & 4u) ? 5u : 0u), r1 = r0 ^ 2u;  // rows of an 8-row group
         uint32_t n = 0;
         const CsTile* rec = record(0);
         ok = rec != nullptr;
@@ -459,22 +461,21 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 if (!ok) break;
             }
             if (!(ok = wait_bounded_warp(BAR(C_V8_FULL0 + b), par, lim))) break;
-            const uint32_t src = base + kCsV8 + b * kCsTile8, dst = base + kCsVf + b * kTileBytes;
-            const uint32_t c16 = lane & 7u;  // 16 dimensions of a key row
-            // the two halves of the row's columns write their 16-byte pieces in opposite order: no bank conflicts
-            const uint32_t flip = c16 >> 2;
+            // Warp wt widens quarter wt. Eight lanes take four 16-byte pieces of two rows r and r ^ 5: in the swizzled
+            // tile of codes and in the swizzled fp16 tile alike they meet eight different bank groups.
+            const uint32_t src = base + kCsV8 + b * kCsTile8 + wt * 4096u;
+            const uint32_t dst = base + kCsVf + b * kTileBytes + (c16 >> 2) * kBoxBytes + wt * 4096u;
+            const uint32_t have = (kv4 >> (8 * wt)) & 255u;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint32_t row = (uint32_t)(i * 16 + wt * 4) + (lane >> 3);
-                uint4 w = ld_shared_v4(src + row * 128u + (c16 << 4));
-                if ((row & 31u) >= ((kv4 >> (8 * (i >> 1))) & 255u)) w = make_uint4(0, 0, 0, 0);
-                const uint32_t at = dst + (c16 >> 2) * kBoxBytes + row * 128u;
+                const uint32_t r = i & 1 ? r1 : r0, at = (uint32_t)(i >> 1) * 1024u + r * 128u;
+                uint4 w = ld_shared_v4(src + at + ((c16 ^ r) << 4));
+                if (have < 32u && (uint32_t)(i >> 1) * 8u + r >= have) w = make_uint4(0, 0, 0, 0);
                 const uint32_t j = 2u * (c16 & 3u);
-                const uint32_t lo0 = flip ? w.z : w.x, lo1 = flip ? w.w : w.y, hi0 = flip ? w.x : w.z, hi1 = flip ? w.y : w.w;
-                st_shared_v4(at + (((j + flip) ^ (row & 7u)) << 4), half2_of_e4m3x2(lo0 & 0xffffu),
-                             half2_of_e4m3x2(lo0 >> 16), half2_of_e4m3x2(lo1 & 0xffffu), half2_of_e4m3x2(lo1 >> 16));
-                st_shared_v4(at + (((j + 1u - flip) ^ (row & 7u)) << 4), half2_of_e4m3x2(hi0 & 0xffffu),
-                             half2_of_e4m3x2(hi0 >> 16), half2_of_e4m3x2(hi1 & 0xffffu), half2_of_e4m3x2(hi1 >> 16));
+                st_shared_v4(dst + at + ((j ^ r) << 4), half2_of_e4m3x2(w.x & 0xffffu), half2_of_e4m3x2(w.x >> 16),
+                             half2_of_e4m3x2(w.y & 0xffffu), half2_of_e4m3x2(w.y >> 16));
+                st_shared_v4(dst + at + (((j + 1u) ^ r) << 4), half2_of_e4m3x2(w.z & 0xffffu),
+                             half2_of_e4m3x2(w.z >> 16), half2_of_e4m3x2(w.w & 0xffffu), half2_of_e4m3x2(w.w >> 16));
             }
             mbar_arrive(BAR(C_V8_EMPTY0 + b));
             fence_proxy_async_smem();
@@ -563,39 +564,45 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             }
             // Row maximum of x over the whole tile, without an exchange between the groups: per 32-key quarter the largest
             // S, then the quarter's scales.
-            auto quarter_max = [&](const float* s, uint32_t have) -> float {
+            auto quarter_max = [](const float* s) -> float {
                 float mx[4];
-                if (have == 32u) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[e] = fmax3(s[e], s[4 + e], s[8 + e]);
+                for (int e = 0; e < 4; ++e) mx[e] = fmax3(s[e], s[4 + e], s[8 + e]);
 #pragma unroll
-                    for (int x = 12; x < 28; x += 8)
+                for (int x = 12; x < 28; x += 8)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) mx[e] = fmax3(mx[e], s[x + e], s[x + 4 + e]);
-                    return fmaxf(fmax3(mx[0], mx[1], fmaxf(s[28], s[29])), fmax3(mx[2], mx[3], fmaxf(s[30], s[31])));
-                }
-                float r = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) r = (uint32_t)e < have ? fmaxf(r, s[e]) : r;
-                return r;
+                    for (int e = 0; e < 4; ++e) mx[e] = fmax3(mx[e], s[x + e], s[x + 4 + e]);
+                return fmaxf(fmax3(mx[0], mx[1], fmaxf(s[28], s[29])), fmax3(mx[2], mx[3], fmaxf(s[30], s[31])));
             };
+            // keys that do not exist become -inf, whatever their codes gave
+            auto hide = [](float* s, uint32_t have) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) s[e] = (uint32_t)e < have ? s[e] : -INFINITY;
+            };
+            const bool whole = kv4 == 0x20202020u;
             float top;
             {
                 float o[64];
                 tmem_ld32(tSb + (grp ^ 1u) * 64u + lane_off, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
                 tmem_ld32(tSb + (grp ^ 1u) * 64u + lane_off + 32u, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
                 tmem_wait_ld();
-                const float m0 = quarter_max(o, (kv4 >> (8 * o0)) & 255u);
-                const float m1 = quarter_max(o + 32, (kv4 >> (8 * o0 + 8)) & 255u);
+                if (!whole) {
+                    hide(o, (kv4 >> (8 * o0)) & 255u);
+                    hide(o + 32, (kv4 >> (8 * o0 + 8)) & 255u);
+                }
+                const float m0 = quarter_max(o), m1 = quarter_max(o + 32);
                 top = fmaxf(fmaf(m0, oks[0] * c, olv[0]), fmaf(m1, oks[1] * c, olv[1]));
             }
             float s[64];
             tmem_ld32(tSb + grp * 64u + lane_off, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
             tmem_ld32(tSb + grp * 64u + lane_off + 32u, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
             tmem_wait_ld();
-            const uint32_t k0 = (kv4 >> (8 * q0)) & 255u, k1 = (kv4 >> (8 * q0 + 8)) & 255u;
+            if (!whole) {
+                hide(s, (kv4 >> (8 * q0)) & 255u);
+                hide(s + 32, (kv4 >> (8 * q0 + 8)) & 255u);
+            }
             {
-                const float m0 = quarter_max(s, k0), m1 = quarter_max(s + 32, k1);
+                const float m0 = quarter_max(s), m1 = quarter_max(s + 32);
                 top = fmaxf(top, fmaxf(fmaf(m0, ks[0] * c, lv[0]), fmaf(m1, ks[1] * c, lv[1])));
             }
             // The reference moves when a row sees its first key, or when the maximum exceeds it by more than 2^8.
@@ -612,28 +619,17 @@ __global__ void __launch_bounds__(kCsThreads, 1)
 #pragma unroll
             for (int qd = 0; qd < 2; ++qd) {
                 const float ck = ks[qd] * c, off = lv[qd] + ref;
-                const uint32_t have = qd ? k1 : k0;
                 float la, lb, lc, ld;
                 uint64_t l2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-                if (have == 32u) {
-                    const uint64_t c2 = f2_pack(ck, ck), o2 = f2_pack(off, off);
+                const uint64_t c2 = f2_pack(ck, ck), o2 = f2_pack(off, off);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const uint64_t xx = f2_fma(f2_pack(s[32 * qd + 2 * e], s[32 * qd + 2 * e + 1]), c2, o2);
-                        float x0, x1;
-                        f2_unpack(xx, x0, x1);
-                        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-                        pw[16 * qd + e] = pack_f16x2(p0, p1);
-                        l2[e & 1] = f2_add(l2[e & 1], f2_pack(p0, p1));
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float p0 = 2u * e < have ? ex2_approx(fmaf(s[32 * qd + 2 * e], ck, off)) : 0.0f;
-                        const float p1 = 2u * e + 1u < have ? ex2_approx(fmaf(s[32 * qd + 2 * e + 1], ck, off)) : 0.0f;
-                        pw[16 * qd + e] = pack_f16x2(p0, p1);
-                        l2[e & 1] = f2_add(l2[e & 1], f2_pack(p0, p1));
-                    }
+                for (int e = 0; e < 16; ++e) {
+                    const uint64_t xx = f2_fma(f2_pack(s[32 * qd + 2 * e], s[32 * qd + 2 * e + 1]), c2, o2);
+                    float x0, x1;
+                    f2_unpack(xx, x0, x1);
+                    const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                    pw[16 * qd + e] = pack_f16x2(p0, p1);
+                    l2[e & 1] = f2_add(l2[e & 1], f2_pack(p0, p1));
                 }
                 f2_unpack(l2[0], la, lb);
                 f2_unpack(l2[1], lc, ld);
