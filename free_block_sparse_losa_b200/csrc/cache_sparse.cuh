@@ -36,7 +36,7 @@
 
 namespace losa {
 
-constexpr int kCsThreads = 512;
+constexpr int kCsThreads = 896;
 constexpr uint32_t kCsTile8 = 128 * 128;                  // a tile of codes
 constexpr int kCsKStages = 3;
 constexpr uint32_t kCsQ = 0;                              // 2 x (q1, q2)
@@ -59,9 +59,9 @@ constexpr int kCsFirst = 1, kCsLast = 2, kCsPre = 4;  // first, last, last but o
 static_assert(sizeof(CsTile) == 80, "tile record");
 
 constexpr uint32_t kCsFac = kCsRec + kCsBatch * kCsBatches * sizeof(CsTile);  // [4][128] reciprocal row factors
-constexpr uint32_t kCsRef = kCsFac + 4 * 128 * 4;    // [4 tiles][128] reference maxima
-constexpr uint32_t kCsDen = kCsRef + 4 * 128 * 4;    // [4 items][128] (denominator, its reference) of the other group
-constexpr uint32_t kCsSmem = kCsDen + 4 * 128 * 8;
+constexpr uint32_t kCsTop = kCsFac + 4 * 128 * 4;    // [4 tiles][2 halves][128] row maxima
+constexpr uint32_t kCsDen = kCsTop + 8 * 128 * 4;    // [2 items][4 groups][128] (denominator, its reference)
+constexpr uint32_t kCsSmem = kCsDen + 8 * 128 * 8;
 static_assert(kCsSmem <= 232448, "shared memory");
 
 enum : uint32_t {
@@ -86,14 +86,39 @@ struct CacheSparseArgs {
     unsigned long long wait_limit_ns;
 };
 
-__device__ __forceinline__ void tc_mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// MMA and commit issued by one elected lane of a converged warp. Descriptors, addresses and barriers must be uniform over
+// the warp and known to be (values from shared memory go through a broadcast shuffle): the operands then stay in uniform
+// registers. Issued by a lone thread in divergent code, each operand is copied there anew, and the issuing thread, not the
+// tensor cores, sets the pace (measured: 1159 us against 950 us on a 4680-token chunk over 32760 keys).
+__device__ __forceinline__ void el_mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                              uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred e, p;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
         ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+__device__ __forceinline__ void el_mma_ts_f16(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void el_commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar) : "memory");
+}
+// Start fetching `bytes` of global memory into L2.
+__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // Instruction descriptor with A and B of format 0 (fp16 for kind::f16, e4m3 for kind::f8f6f4) and fp32 D.
@@ -116,19 +141,21 @@ __global__ void __launch_bounds__(kCsThreads, 1)
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(cs_smem + kCsBar + 47 * 8);
     CsTile* const recs = reinterpret_cast<CsTile*>(cs_smem + kCsRec);
     float* const fac = reinterpret_cast<float*>(cs_smem + kCsFac);
-    float* const refs = reinterpret_cast<float*>(cs_smem + kCsRef);
+    float* const tops = reinterpret_cast<float*>(cs_smem + kCsTop);
     float2* const dens = reinterpret_cast<float2*>(cs_smem + kCsDen);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
     const uint32_t lane = lane_id();
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < C_COUNT; ++s) {
             uint32_t cnt = 1;
             if (s / 2 == C_P_FULL0 / 2 || s / 2 == C_STAGED0 / 2 || s / 2 == C_S_FREE0 / 2 || s / 2 == C_M_READY0 / 2 ||
-                s == C_O_FREE || s / 2 == C_Q_FULL0 / 2 || s / 2 == C_V8_EMPTY0 / 2 || s / 2 == C_VF_FULL0 / 2)
-                cnt = 128;  // a softmax group, or warps 12..15
+                s == C_O_FREE)
+                cnt = 256;  // the two softmax groups of a tile
+            else if (s / 2 == C_Q_FULL0 / 2 || s / 2 == C_V8_EMPTY0 / 2 || s / 2 == C_VF_FULL0 / 2)
+                cnt = 128;  // warps 20..23 or 24..27
             else if (s >= C_REC_EMPTY0 && s < C_REC_EMPTY0 + kCsBatches)
-                cnt = 15;   // every warp but the reader
+                cnt = 27;   // every warp but the reader
             mbar_init(BAR(s), cnt);
         }
         fence_barrier_init();
@@ -145,7 +172,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
     const uint32_t tS = tmem, tO = tmem + 256u, tP = tmem + 384u;
     const unsigned long long lim = a.wait_limit_ns;
 
@@ -163,9 +190,9 @@ __global__ void __launch_bounds__(kCsThreads, 1)
         }
     };
 
-    // Registers: 128 x 56 + 256 x 176 + 128 x 104 is what 512 x 128 were launched with.
+    // Registers: 384 x 40 + 512 x 96 is what 896 x 72 were launched with.
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
         if (warp == 3) {
             // ------------------------------------------------------------------------------------------ reader
             uint32_t bad = 0;
@@ -264,6 +291,8 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 if (g == 0) {
                     rec->qrow = h * a.Np + (q_id - h * a.nq) * kTcRows;
                     rec->flags = q_flags;
+                    if (q_flags >= 0 && (q_flags & kCsFirst))  // warps 24..27 read it some tiles from now
+                        l2_prefetch(a.q + (size_t)rec->qrow * kTcDim, kTileBytes);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR(C_REC_FULL0 + sl));
@@ -313,14 +342,11 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                     ++pv_items;
                 }
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t dV = dV0 + b * (kTileBytes >> 4);
+                const uint64_t dV = dV0 + b * (kTileBytes >> 4);
 #pragma unroll
-                    for (uint32_t kk = 0; kk < 8; ++kk)
-                        tc_mma_ts(tO, tP + b * 64u + kk * 8u, dV + kk * 128u, kIdPV, (first && kk == 0) ? 0u : 1u);
-                    tc_commit(BAR(C_PV_DONE0 + b));
-                }
-                __syncwarp();
+                for (uint32_t kk = 0; kk < 8; ++kk)
+                    el_mma_ts_f16(tO, tP + b * 64u + kk * 8u, dV + kk * 128u, kIdPV, (first && kk == 0) ? 0u : 1u);
+                el_commit(BAR(C_PV_DONE0 + b));
                 ++pv;
                 return true;
             };
@@ -328,7 +354,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             for (;; ++n) {
                 const CsTile* const rec = record(n);
                 if (!(ok = rec != nullptr)) break;
-                const int flags = rec->flags;
+                const int flags = __shfl_sync(0xffffffffu, rec->flags, 0);
                 if (flags < 0) break;
                 release(n);
                 firsts = (firsts & ~(1u << (n & 31u))) | ((uint32_t)(flags & kCsFirst) << (n & 31u));
@@ -341,97 +367,98 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 if (!(ok = wait_bounded_warp(BAR(C_K_FULL0 + ks), (n / kCsKStages) & 1u, lim))) break;
                 if (!(ok = wait_bounded_warp(BAR(C_S_FREE0 + b), ((n >> 1) & 1u) ^ 1u, lim))) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t dQ = dQ0 + qs * (2 * kCsTile8 >> 4), dK = dK0 + ks * (kCsTile8 >> 4);
+                const uint64_t dQ = dQ0 + qs * (2 * kCsTile8 >> 4), dK = dK0 + ks * (kCsTile8 >> 4);
 #pragma unroll
-                    for (uint32_t kk = 0; kk < 8; ++kk)  // four steps of q1, four of q2, over the same K
-                        tc_mma_ss_f8(tS + b * 128u, dQ + (kk >> 2) * (kCsTile8 >> 4) + (kk & 3u) * 2u,
-                                     dK + (kk & 3u) * 2u, kIdQK, kk ? 1u : 0u);
-                    tc_commit(BAR(C_S_FULL0 + b));
-                    tc_commit(BAR(C_K_EMPTY0 + ks));
-                    if (flags & kCsLast) tc_commit(BAR(C_Q_EMPTY0 + qs));
-                }
-                __syncwarp();
+                for (uint32_t kk = 0; kk < 8; ++kk)  // four steps of q1, four of q2, over the same K
+                    el_mma_ss_f8(tS + b * 128u, dQ + (kk >> 2) * (kCsTile8 >> 4) + (kk & 3u) * 2u, dK + (kk & 3u) * 2u,
+                                 kIdQK, kk ? 1u : 0u);
+                el_commit(BAR(C_S_FULL0 + b));
+                el_commit(BAR(C_K_EMPTY0 + ks));
+                if (flags & kCsLast) el_commit(BAR(C_Q_EMPTY0 + qs));
                 if (n >= 2 && !(ok = issue_pv())) break;
             }
             while (ok && pv < n) ok = issue_pv();
-            if (lane == 0) {
-                tc_commit(BAR(C_MMA_DONE));
-                wait_bounded(BAR(C_MMA_DONE), 0, kDrainLimitNs);
-            }
-            __syncwarp();
+            el_commit(BAR(C_MMA_DONE));
+            wait_bounded_warp(BAR(C_MMA_DONE), 0, kDrainLimitNs);
         }
-    } else if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;" ::: "memory");
-        // ------------------------------------------------------------------- Q split, V widening, O stores
-        const int wt = warp - 12;
-        bool fin[2] = {false, false};
-        int32_t fin_row[2] = {0, 0};
-        uint32_t staged[2] = {0, 0}, flushed[2] = {0, 0};
+    } else if (warp >= 24) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
+        // ----------------------------------------------------------------------------------------- Q split
+        // Rows of the block as q1 + q2, swizzled like a TMA tile. Four lanes hold a row, 16 bytes of every 64; the eight
+        // rows of a warp's step are ordered so that 16 lanes' 8-byte stores meet 16 different bank pairs.
+        const uint32_t q4 = lane & 3u, r8 = (((lane >> 2) & 3u) << 1) | (lane >> 4);
         uint32_t items = 0;
-        bool ok = true;
-        // Q rows of the block as q1 + q2, swizzled like a TMA tile; 16 lanes of a warp hold a row.
-        auto split_q = [&](int32_t qrow) -> bool {
+        for (uint32_t n = 0;; ++n) {
+            const CsTile* const rec = record(n);
+            if (!rec || rec->flags < 0) break;
+            const bool first = rec->flags & kCsFirst;
+            const int32_t qrow = rec->qrow;
+            release(n);
+            if (!first) continue;
             const uint32_t qs = items & 1u;
-            if (!wait_bounded_warp(BAR(C_Q_EMPTY0 + qs), ((items >> 1) & 1u) ^ 1u, lim)) return false;
+            if (!wait_bounded_warp(BAR(C_Q_EMPTY0 + qs), ((items >> 1) & 1u) ^ 1u, lim)) break;
             const uint32_t dst = base + kCsQ + qs * 2 * kCsTile8;
-            const uint32_t col = lane & 15u;
-            const __nv_bfloat16* const src = a.q + (size_t)qrow * kTcDim + col * 8;
 #pragma unroll 1
-            for (int part = 0; part < 2; ++part) {
-                uint4 w[8];
+            for (uint32_t i = 0; i < 4; ++i) {
+                const uint32_t row = (uint32_t)(warp - 24) * 32u + i * 8u + r8;
+                const __nv_bfloat16* const src = a.q + ((size_t)qrow + row) * kTcDim + q4 * 8u;
+                uint32_t u[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int row = (part * 8 + i) * 8 + wt * 2 + (int)(lane >> 4);
-                    w[i] = __ldcs(reinterpret_cast<const uint4*>(src + (size_t)row * kTcDim));
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(src + 32 * j));
+                    u[4 * j] = w.x;
+                    u[4 * j + 1] = w.y;
+                    u[4 * j + 2] = w.z;
+                    u[4 * j + 3] = w.w;
                 }
+                // magnitudes of bf16 order as integers; the two halves of a word are compared side by side
+                uint32_t mx = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int row = (part * 8 + i) * 8 + wt * 2 + (int)(lane >> 4);
-                    float f[8];
-                    RopeVec<__nv_bfloat16>::unpack(w[i], f);
-                    uint32_t amax = 0;
+                for (int j = 0; j < 16; ++j) mx = __vmaxu2(mx, u[j] & 0x7fff7fffu);
+                mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float s = row_factor(max(mx & 0xffff0000u, mx << 16));
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t u = __float_as_uint(f[e]) & 0x7fffffffu;
-                        amax = max(amax, u < 0x7f800000u ? u : 0u);
-                    }
-#pragma unroll
-                    for (int x = 8; x; x >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, x));
-                    const float s = row_factor(amax);
+                for (int j = 0; j < 4; ++j) {
                     uint32_t c1[2], c2[2];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        c1[x] = c2[x] = 0;
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const float u0 = f[4 * x + 2 * y] * s, u1 = f[4 * x + 2 * y + 1] * s;
-                            const uint32_t q1 = e4m3x2(u0, u1);
-                            const uint32_t hh = half2_of_e4m3x2(q1);
-                            const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&hh));
-                            c1[x] |= q1 << (16 * y);
-                            c2[x] |= e4m3x2(u0 - z.x, u1 - z.y) << (16 * y);
-                        }
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t v = u[4 * j + x];
+                        const uint32_t h = pack_f16x2(__uint_as_float(v << 16) * s, __uint_as_float(v & 0xffff0000u) * s);
+                        const uint32_t q1 = e4m3x2_of_half2(h);
+                        const uint32_t back = half2_of_e4m3x2(q1);
+                        const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&h),
+                                                     *reinterpret_cast<const __half2*>(&back));
+                        const uint32_t q2 = e4m3x2_of_half2(*reinterpret_cast<const uint32_t*>(&rest));
+                        c1[x >> 1] = x & 1 ? c1[x >> 1] | q1 << 16 : q1;
+                        c2[x >> 1] = x & 1 ? c2[x >> 1] | q2 << 16 : q2;
                     }
-                    const uint32_t at = dst + row * 128u + ((((col >> 1) ^ ((uint32_t)row & 7u)) << 4) | (8u * (col & 1u)));
+                    const uint32_t piece = q4 + 4u * j;  // 8 bytes of the row
+                    const uint32_t at = dst + row * 128u + ((((piece >> 1) ^ (row & 7u)) << 4) | (8u * (piece & 1u)));
                     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(c1[0]), "r"(c1[1]) : "memory");
                     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + kCsTile8), "r"(c2[0]), "r"(c2[1])
                                  : "memory");
-                    // four items deep: the slot of item k is written again for item k + 4, whose split follows P V of item
-                    // k, while Q's two slots only follow Q K^T, which the softmax may not have read yet
-                    if (col == 0) fac[(items & 3u) * 128 + row] = 1.0f / s;
                 }
+                // four items deep: item k's slot is written again for item k + 4, whose split waits for Q K^T of item
+                // k + 2, which waited until item k's last S had been read
+                if (q4 == 0) fac[(items & 3u) * 128u + row] = 1.0f / s;
             }
             fence_proxy_async_smem();
             mbar_arrive(BAR(C_Q_FULL0 + qs));
             ++items;
-            return true;
-        };
+        }
+    } else if (warp >= 20) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
+        // ----------------------------------------------------------------------------- V widening, O stores
+        const int wt = warp - 20;
+        bool fin[2] = {false, false};
+        int32_t fin_row[2] = {0, 0};
+        uint32_t staged[2] = {0, 0}, flushed[2] = {0, 0};
         // The O staged in slot sl leaves for global memory; returns once the slot has been read.
         auto flush = [&](uint32_t sl) -> bool {
             if (!wait_bounded_warp(BAR(C_STAGED0 + sl), staged[sl] & 1u, lim)) return false;
             ++staged[sl];
-            if (warp == 12 && lane == 0) {
+            if (warp == 20 && lane == 0) {
                 tma_store_2d(&tmO, base + kCsVf + sl * kTileBytes, 0, fin_row[sl]);
                 tma_store_2d(&tmO, base + kCsVf + sl * kTileBytes + kBoxBytes, 64, fin_row[sl]);
                 bulk_commit_group();
@@ -444,19 +471,19 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             fin[sl] = false;
             return true;
         };
+        // Warp wt widens quarter wt. Eight lanes take four 16-byte pieces of two rows r and r ^ 5: in the swizzled tile of
+        // codes and in the swizzled fp16 tile alike they meet eight different bank groups.
         const uint32_t c16 = (lane & 3u) | ((lane >> 3) & 1u) << 2;  // 16 dimensions of a key row
         const uint32_t r0 = (lane >> 4) ^ ((lane & 4u) ? 5u : 0u), r1 = r0 ^ 2u;  // rows of an 8-row group
+        bool ok = true;
         uint32_t n = 0;
-        const CsTile* rec = record(0);
-        ok = rec != nullptr;
-        if (ok && rec->flags >= 0) ok = split_q(rec->qrow);
-        while (ok && rec->flags >= 0) {
-            const uint32_t kv4 = rec->kv4;
+        for (;; ++n) {
+            const CsTile* const rec = record(n);
+            if (!(ok = rec != nullptr) || rec->flags < 0) break;
             const bool last = rec->flags & kCsLast;
+            const uint32_t have = (rec->kv4 >> (8 * wt)) & 255u;
             const int32_t qrow = rec->qrow;
-            const CsTile* const next = record(n + 1);
-            if (!(ok = next != nullptr)) break;
-            if (next->flags >= 0 && (next->flags & kCsFirst) && !(ok = split_q(next->qrow))) break;
+            release(n);
             const uint32_t b = n & 1u, par = (n >> 1) & 1u;
             if (n >= 2) {
                 if (fin[b]) ok = flush(b);
@@ -464,11 +491,8 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 if (!ok) break;
             }
             if (!(ok = wait_bounded_warp(BAR(C_V8_FULL0 + b), par, lim))) break;
-            // Warp wt widens quarter wt. Eight lanes take four 16-byte pieces of two rows r and r ^ 5: in the swizzled
-            // tile of codes and in the swizzled fp16 tile alike they meet eight different bank groups.
             const uint32_t src = base + kCsV8 + b * kCsTile8 + wt * 4096u;
             const uint32_t dst = base + kCsVf + b * kTileBytes + (c16 >> 2) * kBoxBytes + wt * 4096u;
-            const uint32_t have = (kv4 >> (8 * wt)) & 255u;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint32_t r = i & 1 ? r1 : r0, at = (uint32_t)(i >> 1) * 1024u + r * 128u;
@@ -485,27 +509,29 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             mbar_arrive(BAR(C_VF_FULL0 + b));
             fin[b] = last;
             fin_row[b] = qrow;
-            release(n);
-            rec = next;
-            ++n;
         }
         for (uint32_t x = 0; ok && x < 2; ++x) {  // the last items' O, oldest slot first
             const uint32_t sl = (n + x) & 1u;
             if (fin[sl]) ok = flush(sl);
         }
-        if (warp == 12 && lane == 0) bulk_wait_all();
+        if (warp == 20 && lane == 0) bulk_wait_all();
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;" ::: "memory");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;" ::: "memory");
         // ----------------------------------------------------------------------------- softmax warpgroups
-        const uint32_t grp = (uint32_t)(warp - 4) >> 2;  // takes tiles n with n & 1 == grp
+        const uint32_t grp = (uint32_t)(warp - 4) >> 2;
+        const uint32_t pair = grp >> 1, half = grp & 1u;  // tiles n with n & 1 == pair; keys 64 half .. 64 half + 63
         const uint32_t wl = (uint32_t)warp & 3u;
         const int row = (int)(wl * 32u + lane);
         const uint32_t lane_off = (wl * 32u) << 16;
-        const uint32_t tSb = tS + grp * 128u + lane_off, tPb = tP + grp * 64u + lane_off, tOb = tO + lane_off;
+        const uint32_t tSb = tS + pair * 128u + half * 64u + lane_off, tPb = tP + pair * 64u + half * 32u + lane_off;
+        const uint32_t tOb = tO + half * 64u + lane_off;
+        // A row's reference after a tile whose maximum is top: it moves when the row sees its first key, or when the
+        // maximum exceeds it by more than 2^8. Every thread of a row follows it through all tiles by itself.
+        auto moved = [](float m, float top) { return m == -INFINITY || top - m > 8.0f ? top : m; };
         uint32_t items = 0;
-        float l = 0.0f, m_l = 0.0f;  // this group's share of the item's denominator, against reference m_l
-        bool fresh = true;           // no tile of this item has come to this group yet
+        float l = 0.0f, m = -INFINITY;  // this thread's share of the item's denominator, and its reference
+        bool fresh = true;              // no tile of this item has come to this pair yet
         for (uint32_t n = 0;; ++n) {
             const CsTile* const rec = record(n);
             if (!rec || rec->flags < 0) break;
@@ -514,76 +540,82 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 ++items;
                 fresh = true;
             }
-            if ((n & 1u) != grp) {
+            if ((n & 1u) != pair) {
                 release(n);
                 continue;
             }
-            const uint32_t kv4 = rec->kv4;
-            const int32_t qrow = rec->qrow;
             const uint32_t par = (n >> 1) & 1u;
-            if (!wait_bounded_warp(BAR(C_S_FULL0 + grp), par, lim)) break;
+            const int32_t qrow = rec->qrow;
+            const uint32_t kv2 = (rec->kv4 >> (16 * half)) & 0xffffu;
+            float ck[2], lv[2], iv[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                ck[x] = rec->ks[2 * half + x];
+                lv[x] = rec->lv[2 * half + x];
+                iv[x] = rec->iv[2 * half + x];
+            }
+            release(n);
+            if (!wait_bounded_warp(BAR(C_S_FULL0 + pair), par, lim)) break;
             tc_fence_after();
+            float s[64];
+            tmem_ld32(tSb, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            tmem_ld32(tSb + 32u, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
             // the row's factor was written before Q K^T could start
             const float c = fmaxf(a.scale_log2 * fac[((items - 1) & 3u) * 128u + (uint32_t)row], 1e-37f);
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive(BAR(C_S_FREE0 + pair));
+            if (kv2 != 0x2020u) {  // keys that do not exist become -inf, whatever their codes gave
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                    s[e] = (uint32_t)(e & 31) < ((kv2 >> (8 * (e >> 5))) & 255u) ? s[e] : -INFINITY;
+            }
             float top = -INFINITY;
-            {
-                float s[128];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) tmem_ld32(tSb + 32u * x, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * x]));
-                tmem_wait_ld();
-                if (kv4 != 0x20202020u) {  // keys that do not exist become -inf, whatever their codes gave
+            for (int x = 0; x < 2; ++x) {
+                const float* const z = s + 32 * x;
+                float mx[4];
 #pragma unroll
-                    for (int e = 0; e < 128; ++e)
-                        s[e] = (uint32_t)(e & 31) < ((kv4 >> (8 * (e >> 5))) & 255u) ? s[e] : -INFINITY;
+                for (int e = 0; e < 4; ++e) mx[e] = fmax3(z[e], z[4 + e], z[8 + e]);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) tmem_st32(tSb + 32u * x, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * x]));
-                    tmem_wait_st();
-                }
+                for (int y = 12; y < 28; y += 8)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float* const z = s + 32 * x;
-                    float mx[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[e] = fmax3(z[e], z[4 + e], z[8 + e]);
-#pragma unroll
-                    for (int y = 12; y < 28; y += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) mx[e] = fmax3(mx[e], z[y + e], z[y + 4 + e]);
-                    const float q =
-                        fmaxf(fmax3(mx[0], mx[1], fmaxf(z[28], z[29])), fmax3(mx[2], mx[3], fmaxf(z[30], z[31])));
-                    top = fmaxf(top, fmaf(q, rec->ks[x] * c, rec->lv[x]));
-                }
+                    for (int e = 0; e < 4; ++e) mx[e] = fmax3(mx[e], z[y + e], z[y + 4 + e]);
+                const float q = fmaxf(fmax3(mx[0], mx[1], fmaxf(z[28], z[29])), fmax3(mx[2], mx[3], fmaxf(z[30], z[31])));
+                ck[x] *= c;
+                top = fmaxf(top, fmaf(q, ck[x], lv[x]));
             }
-            // The reference moves when a row sees its first key, or when the maximum exceeds it by more than 2^8.
-            if (n > 0 && !wait_bounded_warp(BAR(C_M_READY0 + (grp ^ 1u)), ((n - 1) >> 1) & 1u, lim)) break;
-            const float before = (flags & kCsFirst) ? -INFINITY : refs[((n - 1) & 3u) * 128u + (uint32_t)row];
-            float m = before, alpha = 1.0f;
-            if (before == -INFINITY) {
-                m = top;
-            } else if (top - before > 8.0f) {
-                alpha = ex2_approx(before - top);
-                m = top;
+            // The tile before first, then this one: a pair that published a tile before it had seen the other's could run
+            // two phases ahead of a reader.
+            if (n > 0 && !wait_bounded_warp(BAR(C_M_READY0 + (pair ^ 1u)), ((n - 1) >> 1) & 1u, lim)) break;
+            float* const at = tops + (n & 3u) * 256u + (uint32_t)row;
+            at[half * 128u] = top;
+            mbar_arrive(BAR(C_M_READY0 + pair));
+            float before = -INFINITY;
+            if (!(flags & kCsFirst)) {
+                const float* const was = tops + ((n - 1) & 3u) * 256u + (uint32_t)row;
+                before = moved(fresh ? -INFINITY : m, fmaxf(was[0], was[128]));
             }
-            refs[(n & 3u) * 128u + (uint32_t)row] = m;
-            mbar_arrive(BAR(C_M_READY0 + grp));
+            if (!wait_bounded_warp(BAR(C_M_READY0 + pair), par, lim)) break;
+            const float now = moved(before, fmaxf(top, at[(half ^ 1u) * 128u]));
             if (fresh) l = 0.0f;
-            else if (m != m_l) l *= m_l == -INFINITY ? 0.0f : ex2_approx(m_l - m);
+            else if (now != m) l *= m == -INFINITY ? 0.0f : ex2_approx(m - now);
+            const bool rescale = !(flags & kCsFirst) && now != before && before != -INFINITY;
             fresh = false;
-            m_l = m;
+            m = now;
             const float ref = m == -INFINITY ? 0.0f : kCsBias - m;
-            // P's buffer was last read by P V of this group's tile before
-            if (n >= 2 && !wait_bounded_warp(BAR(C_PV_DONE0 + grp), ((n - 2) >> 1) & 1u, lim)) break;
+            // P's buffer was last read by P V of this pair's tile before
+            if (n >= 2 && !wait_bounded_warp(BAR(C_PV_DONE0 + pair), ((n - 2) >> 1) & 1u, lim)) break;
             tc_fence_after();
-            // S is read again, a quarter at a time and one quarter ahead, in a loop of two quarters: unrolled over the row
-            // the two groups and the other warps, each at its own place of the code, starve for instructions.
-            auto weigh = [&](const float (&s)[32], int x) {
-                const float off = rec->lv[x] + ref, ck = rec->ks[x] * c;
-                const uint64_t c2 = f2_pack(ck, ck), o2 = f2_pack(off, off);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float off = lv[x] + ref;
+                const uint64_t c2 = f2_pack(ck[x], ck[x]), o2 = f2_pack(off, off);
                 uint64_t l2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
                 uint32_t pw[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const uint64_t xx = f2_fma(f2_pack(s[2 * e], s[2 * e + 1]), c2, o2);
+                    const uint64_t xx = f2_fma(f2_pack(s[32 * x + 2 * e], s[32 * x + 2 * e + 1]), c2, o2);
                     float x0, x1;
                     f2_unpack(xx, x0, x1);
                     const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
@@ -593,34 +625,16 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 float la, lb, lc, ld;
                 f2_unpack(l2[0], la, lb);
                 f2_unpack(l2[1], lc, ld);
-                l = fmaf((la + lb) + (lc + ld), rec->iv[x], l);
+                l = fmaf((la + lb) + (lc + ld), iv[x], l);
                 tmem_st16(tPb + 16u * x, pw);
-            };
-            {
-                float sa[32], sb[32];
-                tmem_ld32(tSb, *reinterpret_cast<uint32_t(*)[32]>(&sa[0]));
-#pragma unroll 1
-                for (int x = 0; x < 4; x += 2) {
-                    tmem_wait_ld();
-                    tmem_ld32(tSb + 32u * (x + 1), *reinterpret_cast<uint32_t(*)[32]>(&sb[0]));
-                    weigh(sa, x);
-                    tmem_wait_ld();
-                    if (x == 0) {
-                        tmem_ld32(tSb + 64u, *reinterpret_cast<uint32_t(*)[32]>(&sa[0]));
-                    } else {
-                        tc_fence_before();
-                        mbar_arrive(BAR(C_S_FREE0 + grp));
-                    }
-                    weigh(sb, x + 1);
-                }
             }
-            release(n);
             // O is rescaled once P V of tile n - 1 has added to it
-            if (!(flags & kCsFirst) && __any_sync(0xffffffffu, alpha != 1.0f)) {
-                if (!wait_bounded_warp(BAR(C_PV_DONE0 + (grp ^ 1u)), ((n - 1) >> 1) & 1u, lim)) break;
+            if (__any_sync(0xffffffffu, rescale)) {
+                if (!wait_bounded_warp(BAR(C_PV_DONE0 + (pair ^ 1u)), ((n - 1) >> 1) & 1u, lim)) break;
                 tc_fence_after();
+                const float alpha = rescale ? ex2_approx(before - now) : 1.0f;
 #pragma unroll 1
-                for (uint32_t ch = 0; ch < 4; ++ch) {
+                for (uint32_t ch = 0; ch < 2; ++ch) {
                     uint32_t ov[32];
                     tmem_ld32(tOb + ch * 32u, ov);
                     tmem_wait_ld();
@@ -629,42 +643,43 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                     tmem_st32(tOb + ch * 32u, ov);
                 }
             }
-            if (flags & kCsPre) dens[((items - 1) & 3u) * 128u + (uint32_t)row] = make_float2(l, m);
+            float2* const den = dens + ((items - 1) & 1u) * 512u + (uint32_t)row;
+            if (flags & (kCsPre | kCsLast)) den[grp * 128u] = make_float2(l, m);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(BAR(C_P_FULL0 + grp));
+            mbar_arrive(BAR(C_P_FULL0 + pair));
             if (!(flags & kCsLast)) continue;
-            // Epilogue: the item's last P V; the other group's share was written before the P that one waited for.
-            if (!wait_bounded_warp(BAR(C_PV_DONE0 + grp), par, lim)) break;
+            // Epilogue: the item's last P V. The other groups' shares were written before the P that it waited for.
+            if (!wait_bounded_warp(BAR(C_PV_DONE0 + pair), par, lim)) break;
             tc_fence_after();
+            l += den[(grp ^ 1u) * 128u].x;
             if (!(flags & kCsFirst)) {
-                const float2 other = dens[((items - 1) & 3u) * 128u + (uint32_t)row];
-                l += other.y == -INFINITY ? 0.0f : other.x * ex2_approx(other.y - m);
+                const float2 o0 = den[(2u * (pair ^ 1u)) * 128u], o1 = den[(2u * (pair ^ 1u) + 1u) * 128u];
+                l += o0.y == -INFINITY ? 0.0f : (o0.x + o1.x) * ex2_approx(o0.y - m);
             }
             const float inv_l = l == 0.0f ? 0.0f : 1.0f / l;  // a row that saw no key gives zeros
-            uint32_t ov[4][32];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) tmem_ld32(tOb + 32u * x, ov[x]);
+            uint32_t ov[2][32];
+            tmem_ld32(tOb, ov[0]);
+            tmem_ld32(tOb + 32u, ov[1]);
             tmem_wait_ld();
             tc_fence_before();
             mbar_arrive(BAR(C_O_FREE));
-            const uint32_t stage = base + kCsVf + grp * kTileBytes + (uint32_t)row * 128u;
+            const uint32_t stage = base + kCsVf + pair * kTileBytes + half * kBoxBytes + (uint32_t)row * 128u;
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int q4 = 0; q4 < 4; ++q4) {
-                    const uint32_t j = (uint32_t)((x & 1) * 4 + q4);
+                    const uint32_t j = (uint32_t)(x * 4 + q4);
                     uint32_t w[4];
 #pragma unroll
                     for (int k2 = 0; k2 < 4; ++k2)
                         w[k2] = pack_bf16x2(__uint_as_float(ov[x][q4 * 8 + 2 * k2]) * inv_l,
                                             __uint_as_float(ov[x][q4 * 8 + 2 * k2 + 1]) * inv_l);
-                    st_shared_v4(stage + (uint32_t)(x >> 1) * kBoxBytes + ((j ^ ((uint32_t)row & 7u)) << 4), w[0], w[1],
-                                 w[2], w[3]);
+                    st_shared_v4(stage + ((j ^ ((uint32_t)row & 7u)) << 4), w[0], w[1], w[2], w[3]);
                 }
             fence_proxy_async_smem();
-            mbar_arrive(BAR(C_STAGED0 + grp));
-            if (a.lse)
+            mbar_arrive(BAR(C_STAGED0 + pair));
+            if (a.lse && half == 0)
                 a.lse[(size_t)qrow + row] = l == 0.0f ? -INFINITY : (m - kCsBias + lg2_approx(l)) * 0.6931471805599453f;
         }
     }
