@@ -94,27 +94,40 @@ bool make_code_map(CUtensorMap* map, const losa_cache* c, const void* codes, uin
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, bool HALVES>
+// The halves pairing's unit (see rope.cuh): 4, 2 or 1; 0 for the interleaved pairing.
+int rope_unit_width(const losa_rope* r) {
+    if (!r || r->pairing != LOSA_ROPE_HALVES) return 0;
+    const int all = (r->axis_dims[0] | r->axis_dims[1] | r->axis_dims[2]) / 2;
+    return all % 4 == 0 ? 4 : (all % 2 == 0 ? 2 : 1);
+}
+
+template <typename T, int W>
 losa_status launch_rope(const RopeApplyArgs& a, const void* x, void* y, dim3 grid, cudaStream_t stream) {
-    rope_apply_kernel<T, HALVES>
+    rope_apply_kernel<T, W>
         <<<grid, kRopeThreads, 0, stream>>>(a, static_cast<const T*>(x), static_cast<T*>(y));
     return launch_status();
 }
 
-template <typename T, int D, bool HALVES>
-losa_status launch_append(const AppendArgs& a, const void* k, const void* v, dim3 grid, size_t smem,
+template <typename T, int D, int W>
+losa_status launch_append(const AppendArgs& a, const void* k, const void* v, dim3 grid, int threads,
                           cudaStream_t stream) {
-    if (cudaFuncSetAttribute(cache_append_kernel<T, D, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem) != cudaSuccess)
-        return LOSA_ERR_CUDA;
-    cache_append_kernel<T, D, HALVES>
-        <<<grid, kAppendThreads, smem, stream>>>(a, static_cast<const T*>(k), static_cast<const T*>(v));
+    cache_append_kernel<T, D, W><<<grid, threads, 0, stream>>>(a, static_cast<const T*>(k), static_cast<const T*>(v));
     return launch_status();
 }
 
-// Splits of a sequence's keys: enough CTAs for two on every SM, but at least 512 keys for each.
+template <typename T, int D>
+losa_status launch_append_width(int width, const AppendArgs& a, const void* k, const void* v, dim3 grid, int threads,
+                                cudaStream_t stream) {
+    return width == 4   ? launch_append<T, D, 4>(a, k, v, grid, threads, stream)
+           : width == 2 ? launch_append<T, D, 2>(a, k, v, grid, threads, stream)
+           : width == 1 ? launch_append<T, D, 1>(a, k, v, grid, threads, stream)
+                        : launch_append<T, D, 0>(a, k, v, grid, threads, stream);
+}
+
+// Splits of a sequence's keys, of one length for all sequences (by max_len), so that a short sequence has fewer of them and
+// no CTA has more than another. Three rounds of two CTAs per SM even out what is left; a split has at least 512 keys.
 struct AttnPlan {
-    int tiles, splits;
+    int tiles, splits, split_tiles;
     int64_t rows;
     size_t ml_bytes, total;
 };
@@ -126,11 +139,13 @@ AttnPlan attn_plan(const losa_cache* c, int heads, int tokens, int max_len, int 
     const int64_t ctas = (int64_t)c->seqs * c->kv_heads * p.tiles;
     const int64_t cap = (int64_t)c->table_stride * c->page_tokens;
     const int64_t len = max_len <= 0 || max_len > cap ? cap : max_len;
-    int64_t s = 2 * (int64_t)sms / ctas;
+    int64_t s = (6 * (int64_t)sms + ctas - 1) / ctas;
     const int64_t most = (len + 511) / 512;
     if (s > most) s = most;
     if (s > kCaMaxSplits) s = kCaMaxSplits;
-    p.splits = s < 1 ? 1 : (int)s;
+    const int64_t n_tiles = (len + kCaKeys - 1) / kCaKeys;
+    p.split_tiles = (int)((n_tiles + s - 1) / s + kCaWarps - 1) / kCaWarps * kCaWarps;  // whole rounds of the warps
+    p.splits = (int)((n_tiles + p.split_tiles - 1) / p.split_tiles);
     p.rows = (int64_t)c->seqs * tokens * heads;
     p.ml_bytes = p.splits > 1 ? align256((size_t)p.rows * p.splits * sizeof(float2)) : 0;
     p.total = p.splits > 1 ? p.ml_bytes + (size_t)p.rows * p.splits * c->head_dim * sizeof(float) : 0;
@@ -155,7 +170,7 @@ losa_status launch_cache_attn(const losa_cache* c, CacheAttnArgs& a, const AttnP
     if (st != LOSA_OK || p.splits == 1) return st;
     // the join may be scheduled while the splits drain; it waits for their results itself
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.rows + 3) / 4));
+    cfg.gridDim = dim3((unsigned)p.rows);
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
@@ -163,7 +178,7 @@ losa_status launch_cache_attn(const losa_cache* c, CacheAttnArgs& a, const AttnP
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, a, p.rows) != cudaSuccess) return LOSA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, a) != cudaSuccess) return LOSA_ERR_CUDA;
     return launch_status();
 }
 
@@ -200,12 +215,14 @@ losa_status losa_rope_apply(const losa_rope* rope, int32_t dtype, const losa_tok
     a.heads = x_view->heads;
     a.n = x_view->tokens;
     a.n_out = y_view->tokens;
-    a.chunks = rope->head_dim * size / 16;
+    a.d = rope->head_dim;
+    const int width = rope_unit_width(rope);
+    a.units = width ? (a.d + 2 * width - 1) / (2 * width) : a.d * size / 16;
     a.rotate = rotate;
     a.sign = inverse ? -1.0f : 1.0f;
     // One CTA walks all rows of its tokens when the tokens alone fill the GPU four times over; fewer tokens are shared by
     // several CTAs, each with its own angles.
-    const int64_t tokens_ctas = ((int64_t)a.n_out * a.chunks + kRopeThreads - 1) / kRopeThreads;
+    const int64_t tokens_ctas = ((int64_t)a.n_out * a.units + kRopeThreads - 1) / kRopeThreads;
     const int sms = sm_count();
     if (sms <= 0) return LOSA_ERR_CUDA;
     const int rows = a.parts * a.heads;
@@ -214,11 +231,13 @@ losa_status losa_rope_apply(const losa_rope* rope, int32_t dtype, const losa_tok
     a.per_cta = (int)((rows + groups - 1) / groups);
     const dim3 grid((unsigned)tokens_ctas, (unsigned)((rows + a.per_cta - 1) / a.per_cta), (unsigned)a.batch);
     if (grid.y > 65535u) return LOSA_ERR_UNSUPPORTED;
-    const bool halves = rope->pairing == LOSA_ROPE_HALVES;
-    if (dtype == LOSA_DTYPE_BF16)
-        return halves ? launch_rope<__nv_bfloat16, true>(a, x, y, grid, stream)
-                      : launch_rope<__nv_bfloat16, false>(a, x, y, grid, stream);
-    return halves ? launch_rope<float, true>(a, x, y, grid, stream) : launch_rope<float, false>(a, x, y, grid, stream);
+#define LOSA_ROPE(T)                                                       \
+    (width == 4   ? launch_rope<T, 4>(a, x, y, grid, stream)               \
+     : width == 2 ? launch_rope<T, 2>(a, x, y, grid, stream)               \
+     : width == 1 ? launch_rope<T, 1>(a, x, y, grid, stream)               \
+                  : launch_rope<T, 0>(a, x, y, grid, stream))
+    return dtype == LOSA_DTYPE_BF16 ? LOSA_ROPE(__nv_bfloat16) : LOSA_ROPE(float);
+#undef LOSA_ROPE
 }
 
 losa_status losa_cache_append(const losa_cache* cache, const losa_rope* rope, int32_t dtype, const void* k,
@@ -267,7 +286,7 @@ losa_status losa_cache_append(const losa_cache* cache, const losa_rope* rope, in
     a.scale[1] = v_scale;
     if (spans * cache->seqs > 2147483647ll) return LOSA_ERR_UNSUPPORTED;
     // A CTA computes its page's angles once for all its heads; heads are spread over CTAs only as far as the pages leave
-    // SMs idle (two CTAs each, keys and values apart).
+    // SMs idle (keys and values have CTAs of their own).
     const int sms = sm_count();
     if (sms <= 0) return LOSA_ERR_CUDA;
     int64_t groups = ((int64_t)sms + spans * cache->seqs - 1) / (spans * cache->seqs);
@@ -275,16 +294,15 @@ losa_status losa_cache_append(const losa_cache* cache, const losa_rope* rope, in
     a.heads_per_cta = (int)((cache->kv_heads + groups - 1) / groups);
     const dim3 grid((unsigned)(spans * cache->seqs),
                     (unsigned)((cache->kv_heads + a.heads_per_cta - 1) / a.heads_per_cta), 2);
-    const int rows = new_tokens < C ? (new_tokens > 0 ? new_tokens : 1) : C;  // new rows of one page
-    const size_t smem = rope ? (size_t)rows * (cache->head_dim / 2) * sizeof(float2) : 16;
-    const bool halves = rope && rope->pairing == LOSA_ROPE_HALVES;
-#define LOSA_APPEND(T, D)                                                                 \
-    (halves ? launch_append<T, D, true>(a, k, v, grid, smem, stream)                      \
-            : launch_append<T, D, false>(a, k, v, grid, smem, stream))
+    // 16 dimensions a thread: as many warps as the new rows of one page need
+    const int rows = new_tokens < C ? (new_tokens > 0 ? new_tokens : 1) : C;
+    const int threads = ((rows * cache->head_dim / kAppendDims + 127) / 128) * 128;
+    const int width = rope_unit_width(rope);
     if (dtype == LOSA_DTYPE_BF16)
-        return cache->head_dim == 128 ? LOSA_APPEND(__nv_bfloat16, 128) : LOSA_APPEND(__nv_bfloat16, 64);
-    return cache->head_dim == 128 ? LOSA_APPEND(float, 128) : LOSA_APPEND(float, 64);
-#undef LOSA_APPEND
+        return cache->head_dim == 128 ? launch_append_width<__nv_bfloat16, 128>(width, a, k, v, grid, threads, stream)
+                                      : launch_append_width<__nv_bfloat16, 64>(width, a, k, v, grid, threads, stream);
+    return cache->head_dim == 128 ? launch_append_width<float, 128>(width, a, k, v, grid, threads, stream)
+                                  : launch_append_width<float, 64>(width, a, k, v, grid, threads, stream);
 }
 
 size_t losa_cache_attn_workspace_bytes(const losa_cache* cache, int32_t heads, int32_t tokens, int32_t max_len) {
@@ -339,6 +357,7 @@ losa_status losa_cache_attn(const losa_cache* cache, int32_t heads, int32_t toke
     a.causal = causal ? 1 : 0;
     a.tiles = p.tiles;
     a.splits = p.splits;
+    a.split_tiles = p.split_tiles;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.part_ml = static_cast<float2*>(workspace);
     a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.ml_bytes);

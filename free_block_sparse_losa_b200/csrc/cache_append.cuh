@@ -13,7 +13,8 @@
 
 namespace losa {
 
-constexpr int kAppendThreads = 512;
+constexpr int kAppendThreads = 1024;
+constexpr int kAppendDims = 16;  // dimensions of new rows that a thread holds
 constexpr int kCacheExpMin = -40, kCacheExpMax = 60;
 
 // A sequence's pages: the geometry every cache kernel shares.
@@ -63,38 +64,25 @@ __device__ __forceinline__ float cache_scale(uint32_t amax_bits) {
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-template <typename T> __device__ __forceinline__ void load8(const T* p, float (&f)[8]);
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&f)[8]) {
-    RopeVec<__nv_bfloat16>::unpack(__ldcs(reinterpret_cast<const uint4*>(p)), f);
-}
-template <> __device__ __forceinline__ void load8<float>(const float* p, float (&f)[8]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float4 w = __ldcs(reinterpret_cast<const float4*>(p) + i);
-        f[4 * i] = w.x;
-        f[4 * i + 1] = w.y;
-        f[4 * i + 2] = w.z;
-        f[4 * i + 3] = w.w;
-    }
-}
-
 // One CTA takes the new tokens of one page, for the keys (blockIdx.z = 0) or the values, and walks a group of kv heads.
-// K and V are read once and their codes written once, so the kernel is bound by memory; what could cost more is the
-// angles (an angle per token and pair against six bytes of traffic per pair and head), so they are computed once per CTA
-// into shared memory and used for all its heads. A head's rows of the page stay in registers between the maximum over
-// the block and the rounding.
-template <typename T, int D, bool HALVES>
-__global__ void __launch_bounds__(kAppendThreads, 2) cache_append_kernel(const __grid_constant__ AppendArgs a,
-                                                                         const T* __restrict__ k,
-                                                                         const T* __restrict__ v) {
-    constexpr int W = D / 8;                   // 8-element chunks of a row
-    constexpr int ROWS = kAppendThreads / W;   // rows a pass covers
-    constexpr int P = 128 / ROWS;              // passes over the largest page
-    extern __shared__ float2 angle[];          // [new rows of the page][D / 2]: cos, sin
+// K and V are read once and their codes written once, so the kernel is bound by memory. A thread holds the same 16
+// dimensions of the page's rows for every head: their angles stay in registers, computed once (an angle per token and
+// pair against six bytes of traffic per pair and head would cost more than the copy), and the values stay there between the
+// maximum over the block and the rounding. The next head's values are fetched before this head's are used, so that the
+// barrier of the maximum does not drain the memory pipe.
+template <typename T, int D, int W>
+__device__ __forceinline__ void append_page(const AppendArgs& a, const T* __restrict__ src, int64_t ts, int64_t hs,
+                                            uint8_t* __restrict__ code, float* __restrict__ scale, bool keys) {
+    constexpr int N = W ? W : 8;               // dimensions of a unit's side (see rope.cuh)
+    constexpr int SIDES = W ? 2 : 1;
+    constexpr int UNITS = D / (N * SIDES);     // of a row
+    constexpr int P = kAppendDims / (N * SIDES);  // units of a thread
+    constexpr int PAIRS = N * SIDES / 2;
+    constexpr int LOADS = N * sizeof(T) / 16 > 1 ? N * sizeof(T) / 16 : 1;  // fp32, interleaved: two loads a side
+    constexpr int LN = N / LOADS;
     __shared__ uint32_t part[2][kAppendThreads / 32];
 
     const int b = blockIdx.x / a.spans, span = blockIdx.x - b * a.spans;
-    const bool keys = blockIdx.z == 0;
     const int C = a.g.page;
     const int len = a.g.lens[b];
     int m = a.new_tokens;
@@ -132,88 +120,92 @@ __global__ void __launch_bounds__(kAppendThreads, 2) cache_append_kernel(const _
         if (threadIdx.x == 0) atomicOr(&g_device_error, kDevErrBadData);
         return;
     }
-    const int row0 = (int)threadIdx.x / W, e0 = ((int)threadIdx.x % W) * 8;
     const int64_t src0 = first + (int64_t)blk * C - len;        // source row of slot 0
     const bool rotate = keys && a.rotate;
-    if (rotate) {
-        for (int i = threadIdx.x; i < (hi - lo) * (D / 2); i += kAppendThreads) {
-            const int row = i / (D / 2), pair = i - row * (D / 2);
-            const int axis = 2 * pair < a.r.end[0] ? 0 : (2 * pair < a.r.end[1] ? 1 : 2);
-            if (2 * pair < a.r.end[2]) {
-                const int32_t* triple = a.positions ? a.positions + 3 * (src0 + lo + row) : nullptr;
-                const RopePos q = rope_position(a.r, triple, blk * C + lo + row);
-                angle[i] = rope_angle(a.r.step[pair], axis == 0 ? q.p[0] : (axis == 1 ? q.p[1] : q.p[2]));
-            }
-        }
-        __syncthreads();
-    }
-    // where this thread's dimensions find their pair and partner
-    const int turned = rotate ? a.r.end[2] - e0 : 0;
-    int pair[HALVES ? 8 : 1], partner[HALVES ? 8 : 1];
-    uint32_t second = 0;
-    if (HALVES) {
+    const int h0 = blockIdx.y * a.heads_per_cta, h1 = min(a.g.kv_heads, h0 + a.heads_per_cta);
+    const int warps = blockDim.x >> 5;
+
+    // this thread's units: slot and dimensions of each side (slot < 0: none)
+    int slot[P];
+    int dim[P][SIDES];
+    bool turned[P];
+    float2 cs[P][PAIRS];
+    Pack<T, LN> next[P][SIDES][LOADS];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int x = e0 + e;
-            const int ax = x < a.r.end[0] ? 0 : (x < a.r.end[1] ? 1 : 2);
-            const int base = ax == 0 ? 0 : a.r.end[ax - 1], h = a.r.half[ax], l = x - base;
-            const bool f = l < h;
-            second |= f ? 0u : 1u << e;
-            pair[e] = (base >> 1) + (f ? l : l - h);
-            partner[e] = f ? x + h : x - h;
+    for (int p = 0; p < P; ++p) {
+        const int unit = p * (int)blockDim.x + (int)threadIdx.x, row = unit / UNITS, u = unit - row * UNITS;
+        slot[p] = lo + row < hi ? lo + row : -1;
+        dim[p][0] = u * N * SIDES;
+        int pair = dim[p][0];
+        if constexpr (W > 0) {
+            dim[p][1] = dim[p][0] + N;
+            const RopeUnit x = rope_unit<W>(a.r, D, u);  // W > 0 only with a rotation
+            dim[p][0] = x.first;
+            dim[p][1] = x.second;
+            pair = x.pair;
+        }
+        turned[p] = rotate && pair < a.r.end[2];
+#pragma unroll
+        for (int s = 0; s < SIDES; ++s)
+#pragma unroll
+            for (int j = 0; j < LOADS; ++j)
+                if (slot[p] >= 0) next[p][s][j].load(src + (src0 + slot[p]) * ts + h0 * hs + dim[p][s] + j * LN);
+        if (turned[p] && slot[p] >= 0) {
+            const int32_t* triple = a.positions ? a.positions + 3 * (src0 + slot[p]) : nullptr;
+            const RopePos q = rope_position(a.r, triple, blk * C + slot[p]);
+#pragma unroll
+            for (int e = 0; e < PAIRS; ++e) cs[p][e] = rope_pair(a.r, q, pair + 2 * e);
         }
     }
 
-    const T* const src = keys ? k : v;
-    const int64_t ts = keys ? a.k_token : a.v_token, hs = keys ? a.k_head : a.v_head;
-    uint8_t* const code = a.code[keys ? 0 : 1];
-    float* const scale = a.scale[keys ? 0 : 1];
-    const int h0 = blockIdx.y * a.heads_per_cta, h1 = min(a.g.kv_heads, h0 + a.heads_per_cta);
     for (int h = h0; h < h1; ++h) {
-        float f[P][8];
+        float f[P][SIDES][N];
         uint32_t amax = 0;
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const int slot = lo + p * ROWS + row0;
-            if (slot < hi) load8(src + (src0 + slot) * ts + h * hs + e0, f[p]);
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int s = 0; s < SIDES; ++s)
+#pragma unroll
+                for (int e = 0; e < N; ++e) f[p][s][e] = slot[p] >= 0 ? next[p][s][e / LN].get(e % LN) : 0.0f;
+        if (h + 1 < h1) {
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int s = 0; s < SIDES; ++s)
+#pragma unroll
+                    for (int j = 0; j < LOADS; ++j)
+                        if (slot[p] >= 0)
+                            next[p][s][j].load(src + (src0 + slot[p]) * ts + (h + 1) * hs + dim[p][s] + j * LN);
         }
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int slot = lo + p * ROWS + row0;
-            if (slot >= hi) continue;
-            if (turned > 0) {
-                const float2* const row = angle + (slot - lo) * (D / 2);
-                if (HALVES) {
-                    const T* const g = src + (src0 + slot) * ts + h * hs;
+            if (turned[p]) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (e < turned) {
-                            const float2 cs = row[pair[e]];
-                            f[p][e] = fmaf((second >> e) & 1u ? cs.y : -cs.y, RopeVec<T>::one(g + partner[e]),
-                                           cs.x * f[p][e]);
-                        }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2)
-                        if (e < turned) {
-                            const float2 cs = row[(e0 + e) >> 1];
-                            const float x0 = f[p][e], x1 = f[p][e + 1];
-                            f[p][e] = fmaf(-cs.y, x1, cs.x * x0);
-                            f[p][e + 1] = fmaf(cs.y, x0, cs.x * x1);
-                        }
+                for (int e = 0; e < PAIRS; ++e) {
+                    float& z0 = f[p][0][W ? e : 2 * e];
+                    float& z1 = f[p][SIDES - 1][W ? e : 2 * e + 1];
+                    const float x0 = z0, x1 = z1;
+                    const float2 q = cs[p][e];
+                    // interleaved units may end in dimensions that are not rotated (q = (1, 0)): they must not meet their
+                    // neighbour's infinity
+                    z0 = q.y == 0.0f ? q.x * x0 : fmaf(-q.y, x1, q.x * x0);
+                    z1 = q.y == 0.0f ? q.x * x1 : fmaf(q.y, x0, q.x * x1);
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t u = __float_as_uint(f[p][e]) & 0x7fffffffu;
-                amax = max(amax, u < 0x7f800000u ? u : 0u);  // infinities saturate, NaN stays NaN: neither sets a scale
-            }
+            for (int s = 0; s < SIDES; ++s)
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const uint32_t u = __float_as_uint(f[p][s][e]) & 0x7fffffffu;
+                    amax = max(amax, u < 0x7f800000u ? u : 0u);  // infinities saturate, NaN stays: neither sets a scale
+                }
         }
         amax = __reduce_max_sync(0xffffffffu, amax);
         uint32_t* const buf = part[h & 1];
         if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = amax;
         __syncthreads();  // the other buffer is free: every thread read it before this barrier
-        amax = __reduce_max_sync(0xffffffffu, buf[threadIdx.x & (kAppendThreads / 32 - 1)]);
+        const int lane = threadIdx.x & 31;
+        amax = __reduce_max_sync(0xffffffffu, lane < warps ? buf[lane] : 0u);
         const int64_t at = (int64_t)page * a.g.kv_heads + h;
         float sc = cache_scale(amax);
         uint8_t* const dst = code + at * C * D;
@@ -221,7 +213,7 @@ __global__ void __launch_bounds__(kAppendThreads, 2) cache_append_kernel(const _
             const float old = scale[at];
             if (sc > old) {
                 const float ratio = old / sc;
-                for (int i = threadIdx.x; i < lo * W; i += kAppendThreads) {
+                for (int i = threadIdx.x; i < lo * (D / 8); i += blockDim.x) {
                     uint2 w = *reinterpret_cast<const uint2*>(dst + i * 8);
                     uint32_t u[2] = {w.x, w.y};
 #pragma unroll
@@ -229,7 +221,7 @@ __global__ void __launch_bounds__(kAppendThreads, 2) cache_append_kernel(const _
                         uint32_t o = 0;
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
-                            const uint32_t hh = half2_of_e4m3x2(u[j] >> (16 * s));
+                            const uint32_t hh = half2_of_e4m3x2((u[j] >> (16 * s)) & 0xffffu);
                             const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&hh));
                             o |= e4m3x2(z.x * ratio, z.y * ratio) << (16 * s);
                         }
@@ -246,16 +238,38 @@ __global__ void __launch_bounds__(kAppendThreads, 2) cache_append_kernel(const _
         const float inv = 1.0f / sc;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int slot = lo + p * ROWS + row0;
-            if (slot >= hi) continue;
-            uint32_t u[2];
+            if (slot[p] < 0) continue;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                u[j] = e4m3x2(f[p][4 * j] * inv, f[p][4 * j + 1] * inv) |
-                       (e4m3x2(f[p][4 * j + 2] * inv, f[p][4 * j + 3] * inv) << 16);
-            *reinterpret_cast<uint2*>(dst + (int64_t)slot * D + e0) = make_uint2(u[0], u[1]);
+            for (int s = 0; s < SIDES; ++s) {
+                uint8_t* const to = dst + (int64_t)slot[p] * D + dim[p][s];
+                const float (&g)[N] = f[p][s];
+                if constexpr (N == 8) {
+                    uint32_t u[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        u[j] = e4m3x2(g[4 * j] * inv, g[4 * j + 1] * inv) |
+                               (e4m3x2(g[4 * j + 2] * inv, g[4 * j + 3] * inv) << 16);
+                    *reinterpret_cast<uint2*>(to) = make_uint2(u[0], u[1]);
+                } else if constexpr (N == 4) {
+                    *reinterpret_cast<uint32_t*>(to) =
+                        e4m3x2(g[0] * inv, g[1] * inv) | (e4m3x2(g[2] * inv, g[3] * inv) << 16);
+                } else if constexpr (N == 2) {
+                    *reinterpret_cast<uint16_t*>(to) = (uint16_t)e4m3x2(g[0] * inv, g[1] * inv);
+                } else {
+                    *to = (uint8_t)e4m3x2(g[0] * inv, 0.0f);
+                }
+            }
         }
     }
+}
+
+// Values, and keys that are not rotated, need no pairs: they take the widest loads whatever the pairing.
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(kAppendThreads, 1) cache_append_kernel(const __grid_constant__ AppendArgs a,
+                                                                         const T* __restrict__ k,
+                                                                         const T* __restrict__ v) {
+    if (blockIdx.z == 0) append_page<T, D, W>(a, k, a.k_token, a.k_head, a.code[0], a.scale[0], true);
+    else append_page<T, D, 0>(a, v, a.v_token, a.v_head, a.code[1], a.scale[1], false);
 }
 
 }  // namespace losa

@@ -24,7 +24,7 @@ constexpr int kCaWarps = 4;
 constexpr int kCaStages = 3;   // tiles in flight per warp
 constexpr int kCaKeys = 32;    // keys of a warp's tile: never more than one page
 constexpr int kCaRows = 16;    // query rows of a CTA
-constexpr int kCaMaxSplits = 64;
+constexpr int kCaMaxSplits = 128;
 constexpr float kCaBias = 10.0f;
 
 struct CacheAttnArgs {
@@ -37,7 +37,7 @@ struct CacheAttnArgs {
     int64_t q_seq, q_token, q_head, o_seq, o_token, o_head;
     int heads, group, tokens, causal;
     int tiles;                 // 16-row tiles of a (sequence, kv head)
-    int splits;
+    int splits, split_tiles;   // splits of a sequence, 32-key tiles of each (the last one takes what is left)
     float scale_log2;
     float* part_o;             // [row][split][D]
     float2* part_ml;           // [row][split]: maximum, denominator
@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(kCaWarps * 32, 2)
         len = len < 0 ? 0 : (int)room;
     }
     const int n_tiles = (len + kCaKeys - 1) / kCaKeys;
-    const int t0 = (int)((int64_t)n_tiles * split / a.splits), t1 = (int)((int64_t)n_tiles * (split + 1) / a.splits);
+    const int t0 = min(n_tiles, split * a.split_tiles);
+    const int t1 = split == a.splits - 1 ? n_tiles : min(n_tiles, t0 + a.split_tiles);
     const int mine = max(0, (t1 - t0 - warp + kCaWarps - 1) / kCaWarps);  // this warp's tiles: t0 + warp, + 4, ...
 
     if (lane == 0) {
@@ -375,15 +376,16 @@ __global__ void __launch_bounds__(kCaWarps * 32, 2)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Joins the splits of every row: one warp per row, the partial results weighted by 2^(their maximum - the row's).
+// Joins the splits of every row, weighted by 2^(their maximum - the row's): one CTA per row, a warp for every fourth split.
 template <int D>
-__global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ CacheAttnArgs a, int64_t rows) {
+__global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ CacheAttnArgs a) {
+    constexpr int E = D / 32;
+    __shared__ float sum[4][D], dens[4];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (id >= rows) return;
+    const int64_t id = blockIdx.x;
+    const int warp = threadIdx.x >> 5;
     const uint32_t lane = lane_id();
     const float2* const ml = a.part_ml + id * a.splits;
-    constexpr int E = D / 32;
     float top = -INFINITY;
     for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, ml[s].x);
 #pragma unroll
@@ -391,21 +393,31 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
     float den = 0.0f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    for (int s = 0; s < a.splits; ++s) {
+#pragma unroll 4
+    for (int s = warp; s < a.splits; s += 4) {
         const float2 p = ml[s];
         const float f = p.x == -INFINITY ? 0.0f : ex2_approx(p.x - top);
-        const float* const src = a.part_o + (id * a.splits + s) * D + lane * E;
+        const float* const src = a.part_o + (id * a.splits + s) * D + lane;
         den = fmaf(p.y, f, den);
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(src[e], f, o[e]);
+        for (int e = 0; e < E; ++e) o[e] = fmaf(src[32 * e], f, o[e]);
     }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[warp][lane + 32 * e] = o[e];
+    if (lane == 0) dens[warp] = den;
+    __syncthreads();
+    den = (dens[0] + dens[1]) + (dens[2] + dens[3]);
     const int64_t tok = id / a.heads;
     const int head = (int)(id - tok * a.heads), seq = (int)(tok / a.tokens), token = (int)(tok - (int64_t)seq * a.tokens);
-    const float inv = top == -INFINITY ? 0.0f : 1.0f / den;
-    __nv_bfloat16* const dst = a.o + seq * a.o_seq + token * a.o_token + head * a.o_head + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-    if (a.lse && lane == 0)
+    if (threadIdx.x < D / 2) {
+        const int d = 2 * threadIdx.x;
+        const float inv = top == -INFINITY ? 0.0f : 1.0f / den;
+        const float u = (sum[0][d] + sum[1][d]) + (sum[2][d] + sum[3][d]);
+        const float v = (sum[0][d + 1] + sum[1][d + 1]) + (sum[2][d + 1] + sum[3][d + 1]);
+        *reinterpret_cast<uint32_t*>(a.o + seq * a.o_seq + token * a.o_token + head * a.o_head + d) =
+            pack_bf16x2(u * inv, v * inv);
+    }
+    if (a.lse && threadIdx.x == 0)
         a.lse[id] = top == -INFINITY ? -INFINITY : (top - kCaBias + __log2f(den)) * 0.6931471805599453f;
 }
 
