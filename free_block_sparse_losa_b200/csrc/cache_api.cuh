@@ -124,10 +124,12 @@ losa_status launch_append_width(int width, const AppendArgs& a, const void* k, c
                         : launch_append<T, D, 0>(a, k, v, grid, threads, stream);
 }
 
-// Splits of a sequence's keys, of one length for all sequences (by max_len), so that a short sequence has fewer of them and
-// no CTA has more than another. Three rounds of two CTAs per SM even out what is left; a split has at least 512 keys.
+// Where every sequence is short (max_len), or there is no more than one unit's worth of CTAs to gain, a CTA takes a unit and
+// there is nothing to join: up to 1024 keys the join would cost more than it saves (a warp then has eight tiles). Otherwise
+// two CTAs per SM share all units' keys in equal ranges; a unit, at most 1 / (kv heads x row tiles) of the work, lies in at
+// most CTAs / (kv heads x row tiles) + 2 of them, and in at most kCaMaxSplits (see ca_work).
 struct AttnPlan {
-    int tiles, splits, split_tiles;
+    int tiles, splits, ctas;
     int64_t rows;
     size_t ml_bytes, total;
 };
@@ -136,19 +138,20 @@ AttnPlan attn_plan(const losa_cache* c, int heads, int tokens, int max_len, int 
     AttnPlan p;
     const int64_t rows = (int64_t)tokens * (heads / c->kv_heads);
     p.tiles = (int)((rows + kCaRows - 1) / kCaRows);
-    const int64_t ctas = (int64_t)c->seqs * c->kv_heads * p.tiles;
+    p.rows = (int64_t)c->seqs * tokens * heads;
+    const int64_t units = (int64_t)c->kv_heads * p.tiles;
     const int64_t cap = (int64_t)c->table_stride * c->page_tokens;
     const int64_t len = max_len <= 0 || max_len > cap ? cap : max_len;
-    int64_t s = (6 * (int64_t)sms + ctas - 1) / ctas;
-    const int64_t most = (len + 511) / 512;
-    if (s > most) s = most;
+    p.ml_bytes = p.total = 0;
+    p.splits = 0;
+    p.ctas = (int)(units * c->seqs);
+    if (len <= 1024 || units * c->seqs > (1 << 20)) return p;
+    p.ctas = 2 * sms;
+    int64_t s = (p.ctas + units - 1) / units + 2;
     if (s > kCaMaxSplits) s = kCaMaxSplits;
-    const int64_t n_tiles = (len + kCaKeys - 1) / kCaKeys;
-    p.split_tiles = (int)((n_tiles + s - 1) / s + kCaWarps - 1) / kCaWarps * kCaWarps;  // whole rounds of the warps
-    p.splits = (int)((n_tiles + p.split_tiles - 1) / p.split_tiles);
-    p.rows = (int64_t)c->seqs * tokens * heads;
-    p.ml_bytes = p.splits > 1 ? align256((size_t)p.rows * p.splits * sizeof(float2)) : 0;
-    p.total = p.splits > 1 ? p.ml_bytes + (size_t)p.rows * p.splits * c->head_dim * sizeof(float) : 0;
+    p.splits = (int)s;
+    p.ml_bytes = align256((size_t)p.rows * p.splits * sizeof(float2));
+    p.total = p.ml_bytes + (size_t)p.rows * p.splits * c->head_dim * sizeof(float);
     return p;
 }
 
@@ -164,10 +167,9 @@ losa_status launch_cache_attn(const losa_cache* c, CacheAttnArgs& a, const AttnP
     if (cudaFuncSetAttribute(cache_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)kCaSmem<D>) != cudaSuccess)
         return LOSA_ERR_CUDA;
-    const dim3 grid((unsigned)p.splits, (unsigned)(c->kv_heads * p.tiles), (unsigned)c->seqs);
-    cache_attn_kernel<D><<<grid, kCaWarps * 32, kCaSmem<D>, stream>>>(tk, tv, a);
+    cache_attn_kernel<D><<<p.ctas, kCaWarps * 32, kCaSmem<D>, stream>>>(tk, tv, a);
     const losa_status st = launch_status();
-    if (st != LOSA_OK || p.splits == 1) return st;
+    if (st != LOSA_OK || p.splits == 0) return st;
     // the join may be scheduled while the splits drain; it waits for their results itself
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.rows);
@@ -178,7 +180,7 @@ losa_status launch_cache_attn(const losa_cache* c, CacheAttnArgs& a, const AttnP
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, a) != cudaSuccess) return LOSA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, a, p.ctas) != cudaSuccess) return LOSA_ERR_CUDA;
     return launch_status();
 }
 
@@ -333,7 +335,7 @@ losa_status losa_cache_attn(const losa_cache* cache, int32_t heads, int32_t toke
     const int sms = sm_count();
     if (sms <= 0) return LOSA_ERR_CUDA;
     const AttnPlan p = attn_plan(cache, heads, tokens, max_len, sms);
-    if ((int64_t)cache->kv_heads * p.tiles > 65535) return LOSA_ERR_UNSUPPORTED;
+    if ((int64_t)cache->kv_heads * p.tiles * cache->seqs > 2147483647ll) return LOSA_ERR_UNSUPPORTED;
     if (p.total > 0) {
         if (!aligned16(workspace)) return LOSA_ERR_INVALID_ARG;
         if (ws_bytes < p.total) return LOSA_ERR_CAPACITY;
@@ -357,7 +359,7 @@ losa_status losa_cache_attn(const losa_cache* cache, int32_t heads, int32_t toke
     a.causal = causal ? 1 : 0;
     a.tiles = p.tiles;
     a.splits = p.splits;
-    a.split_tiles = p.split_tiles;
+    a.seqs = cache->seqs;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.part_ml = static_cast<float2*>(workspace);
     a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.ml_bytes);

@@ -37,7 +37,8 @@ struct CacheAttnArgs {
     int64_t q_seq, q_token, q_head, o_seq, o_token, o_head;
     int heads, group, tokens, causal;
     int tiles;                 // 16-row tiles of a (sequence, kv head)
-    int splits, split_tiles;   // splits of a sequence, 32-key tiles of each (the last one takes what is left)
+    int seqs;
+    int splits;                // 0: one CTA per unit; else the most CTAs that share a unit
     float scale_log2;
     float* part_o;             // [row][split][D]
     float2* part_ml;           // [row][split]: maximum, denominator
@@ -78,6 +79,50 @@ __device__ __forceinline__ float row_factor(uint32_t amax_bits) {
     return e == 0 ? 1.0f : __uint_as_float((uint32_t)min(max(127 + 127 + 7 - e, 1), 254) << 23);
 }
 
+// The work of a call. A unit is a (sequence, kv head, row tile); its work is its sequence's 32-key tiles. The units' tiles,
+// one behind the other, are cut into equal ranges, one per CTA, across the units' borders: ragged lengths and any number of
+// heads load every SM alike (cutting each sequence by itself left a third of the time idle: 127 against 83 us on eight
+// ragged streams). A unit that lies in several ranges is joined by cache_join_kernel. Every CTA finds its place in the
+// lengths by itself.
+struct CaWork {
+    int64_t total, range;  // tiles of the call; of a CTA
+};
+
+__device__ __forceinline__ int ca_tiles_of(const CacheAttnArgs& a, int seq, int& len) {
+    const int64_t room = (int64_t)a.g.table_stride * a.g.page;
+    len = a.g.lens[seq];
+    if (len < 0 || len > room) len = len < 0 ? 0 : (int)room;  // reported where the sequence's page table is read
+    return (len + kCaKeys - 1) / kCaKeys;
+}
+
+// Total and range; with seq >= 0 also the tiles before that sequence. Called by a whole warp.
+__device__ __forceinline__ CaWork ca_work(const CacheAttnArgs& a, int ctas, int seq, int64_t& before) {
+    const int units = a.g.kv_heads * a.tiles;
+    int64_t sum = 0, head = 0;
+    int most = 0;
+    for (int b = (int)lane_id(); b < a.seqs; b += 32) {
+        int len;
+        const int t = ca_tiles_of(a, b, len);
+        sum += t;
+        if (b < seq) head += t;
+        most = max(most, t);
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        head += __shfl_xor_sync(0xffffffffu, head, x);
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, x));
+    }
+    before = head * units;
+    CaWork w;
+    w.total = sum * units;
+    w.range = (w.total + ctas - 1) / ctas;
+    // at least eight tiles for each warp pair of loads to pay, and no unit in more than `splits` ranges
+    const int64_t least = a.splits > 2 ? ((int64_t)most + a.splits - 3) / (a.splits - 2) : most;
+    w.range = max(max(w.range, least), (int64_t)(2 * kCaWarps));
+    return w;
+}
+
 // Row of an 8-key group that column n of an S tile stands for. Any order is right as long as S, P and V agree; this one
 // lets the eight lanes of a shared-memory phase read eight different 16-byte columns of the swizzled K and V tiles.
 __device__ __forceinline__ int key_of_column(int n) { return (n & 1) ? ((n - 1) ^ 4) | 1 : n; }
@@ -112,30 +157,68 @@ __global__ void __launch_bounds__(kCaWarps * 32, 2)
     float2* const tile_scale = reinterpret_cast<float2*>(smem + BARS + kCaWarps * kCaStages * 8) + warp * kCaStages;
     float2* const row_ml = reinterpret_cast<float2*>(smem + BARS + kCaWarps * kCaStages * 16);
 
-    const int split = blockIdx.x;
-    const int tile = blockIdx.y % a.tiles, kvh = blockIdx.y / a.tiles;
-    const int seq = blockIdx.z;
     const int C = a.g.page;
-    const int64_t room = (int64_t)a.g.table_stride * C;
-    int len = a.g.lens[seq];
-    if (len < 0 || len > room) {
-        if (threadIdx.x == 0) atomicOr(&g_device_error, kDevErrBadData);
-        len = len < 0 ? 0 : (int)room;
-    }
-    const int n_tiles = (len + kCaKeys - 1) / kCaKeys;
-    const int t0 = min(n_tiles, split * a.split_tiles);
-    const int t1 = split == a.splits - 1 ? n_tiles : min(n_tiles, t0 + a.split_tiles);
-    const int mine = max(0, (t1 - t0 - warp + kCaWarps - 1) / kCaWarps);  // this warp's tiles: t0 + warp, + 4, ...
-
+    const int units = a.g.kv_heads * a.tiles;
     if (lane == 0) {
         for (int s = 0; s < kCaStages; ++s) mbar_init(bar + 8 * s, 1);
         fence_barrier_init();
     }
     __syncwarp();
 
+    // This CTA's range of the call's tiles, and the sequence it starts in.
+    int64_t pos, stop, range = 1, seq_pos = 0;  // seq_pos: first tile of sequence seq
+    int seq = 0, len, n_tiles;
+    if (a.splits == 0) {
+        seq = blockIdx.x / units;
+        n_tiles = ca_tiles_of(a, seq, len);
+        seq_pos = 0;
+        pos = (int64_t)(blockIdx.x - seq * units) * n_tiles;
+        stop = pos + n_tiles;
+        if (a.g.lens[seq] != len && threadIdx.x == 0) atomicOr(&g_device_error, kDevErrBadData);
+        if (n_tiles == 0) stop = pos + 1;  // one round without keys writes the rows
+    } else {
+        const CaWork w = ca_work(a, gridDim.x, 0, seq_pos);
+        range = w.range;
+        pos = (int64_t)blockIdx.x * range;
+        stop = min(w.total, pos + range);
+        if (pos >= stop) return;
+        // the sequence that holds tile pos < total: 32 sequences at a time
+        seq_pos = 0;
+        for (;; seq += 32) {
+            int64_t upto = seq + (int)lane < a.seqs ? (int64_t)ca_tiles_of(a, seq + (int)lane, len) * units : 0;
+            const int64_t own = upto;
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, upto, x);
+                if ((int)lane >= x) upto += y;
+            }
+            const uint32_t behind = __ballot_sync(0xffffffffu, pos < seq_pos + upto);
+            if (behind) {
+                const int l = __ffs(behind) - 1;
+                seq_pos += __shfl_sync(0xffffffffu, upto - own, l);
+                seq += l;
+                break;
+            }
+            seq_pos += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        n_tiles = ca_tiles_of(a, seq, len);
+    }
+    uint32_t filled = 0;  // tiles this warp has issued so far: stage and phase of the next
+    while (pos < stop) {
+    while (a.splits != 0 && pos >= seq_pos + (int64_t)n_tiles * units) {
+        seq_pos += (int64_t)n_tiles * units;
+        n_tiles = ca_tiles_of(a, ++seq, len);
+    }
+    const int unit = n_tiles == 0 ? (int)(blockIdx.x % units) : (int)((pos - seq_pos) / n_tiles);
+    const int tile = unit % a.tiles, kvh = unit / a.tiles;
+    const int64_t unit_pos = seq_pos + (int64_t)unit * n_tiles;
+    const int t0 = (int)(pos - unit_pos), t1 = n_tiles == 0 ? 0 : (int)min((int64_t)n_tiles, stop - unit_pos);
+    const int mine = max(0, (t1 - t0 - warp + kCaWarps - 1) / kCaWarps);  // this warp's tiles: t0 + warp, + 4, ...
+
     // Page and scales of the next 32 tiles, one tile per lane; a bad page is reported and its keys do not exist.
     int at_row = 0;
     float at_ks = 1.0f, at_vs = 1.0f;
+    const uint32_t base_fill = filled;
     auto issue = [&](int j) {
         if ((j & 31) == 0) {
             const int i = j + (int)lane;
@@ -156,13 +239,14 @@ __global__ void __launch_bounds__(kCaWarps * 32, 2)
         }
         const int row = __shfl_sync(0xffffffffu, at_row, j & 31);
         const float ks = __shfl_sync(0xffffffffu, at_ks, j & 31), vs = __shfl_sync(0xffffffffu, at_vs, j & 31);
+        const uint32_t s = (base_fill + j) % kCaStages;
         if (lane == 0) {
-            const int s = j % kCaStages;
             tile_scale[s] = make_float2(row < 0 ? -1.0f : ks, vs);
             mbar_arrive_expect_tx(bar + 8 * s, 2 * TILE);
             tma_load_2d(ring + s * 2 * TILE, &tmK, 0, max(row, 0), bar + 8 * s);
             tma_load_2d(ring + s * 2 * TILE + TILE, &tmV, 0, max(row, 0), bar + 8 * s);
         }
+        ++filled;
     };
     for (int j = 0; j < kCaStages && j < mine; ++j) issue(j);
 
@@ -215,8 +299,8 @@ __global__ void __launch_bounds__(kCaWarps * 32, 2)
     bool ok = true;
     int j = 0;
     for (; j < mine; ++j) {
-        const int s = j % kCaStages;
-        if (!(ok = wait_bounded_warp(bar + 8 * s, (uint32_t)(j / kCaStages) & 1u, a.wait_limit_ns))) break;
+        const uint32_t f = base_fill + j, s = f % kCaStages;
+        if (!(ok = wait_bounded_warp(bar + 8 * s, (f / kCaStages) & 1u, a.wait_limit_ns))) break;
         const float2 sc = tile_scale[s];  // written before the arrival this wait has seen
         const uint32_t tk = ring + s * 2 * TILE, tv = tk + TILE;
         const int key0 = (t0 + warp + j * kCaWarps) * kCaKeys;
@@ -323,8 +407,8 @@ __global__ void __launch_bounds__(kCaWarps * 32, 2)
         if (j + kCaStages < mine) issue(j + kCaStages);
     }
     if (!ok)  // copies in flight land before the ring is used for anything else
-        for (int x = j; x < mine && x < j + kCaStages; ++x)
-            wait_bounded_warp(bar + 8 * (x % kCaStages), (uint32_t)(x / kCaStages) & 1u, kDrainLimitNs);
+        for (uint32_t x = base_fill + j; x != filled; ++x)
+            wait_bounded_warp(bar + 8 * (x % kCaStages), (x / kCaStages) & 1u, kDrainLimitNs);
 
     // Join the four warps through their own rings: [16 rows][D] fp32 each.
 #pragma unroll
@@ -340,6 +424,7 @@ __global__ void __launch_bounds__(kCaWarps * 32, 2)
 #pragma unroll
         for (int i = 0; i < 4; ++i) mine_o[(g + 8 * (i >> 1)) * D + NT * (2 * t + (i & 1)) + n] = acc[n][i];
     __syncthreads();
+    const bool shared = a.splits != 0 && t1 - t0 < n_tiles;  // other CTAs hold the rest of the unit
     for (int i = threadIdx.x; i < kCaRows * (D / 4); i += kCaWarps * 32) {
         const int r = i / (D / 4), d0 = (i - r * (D / 4)) * 4;
         const int row = tile * kCaRows + r;
@@ -361,8 +446,8 @@ __global__ void __launch_bounds__(kCaWarps * 32, 2)
         }
         const int token = row / a.group, head = kvh * a.group + row % a.group;
         const int64_t id = ((int64_t)seq * a.tokens + token) * a.heads + head;
-        if (a.splits > 1) {
-            const int64_t at = id * a.splits + split;
+        if (shared) {
+            const int64_t at = id * a.splits + (int)(blockIdx.x - unit_pos / range);
             *reinterpret_cast<float4*>(a.part_o + at * D + d0) = make_float4(o[0], o[1], o[2], o[3]);
             if (d0 == 0) a.part_ml[at] = make_float2(top, den);
         } else {
@@ -373,28 +458,45 @@ __global__ void __launch_bounds__(kCaWarps * 32, 2)
                 a.lse[id] = top == -INFINITY ? -INFINITY : (top - kCaBias + __log2f(den)) * 0.6931471805599453f;
         }
     }
+    pos += max(t1 - t0, 1);
+    if (!__syncthreads_and(ok)) break;  // the rings are free again; after a timeout every warp stops
+    fence_proxy_async_smem();
+    }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Joins the splits of every row, weighted by 2^(their maximum - the row's): one CTA per row, a warp for every fourth split.
+// Joins the ranges that share a unit, weighted by 2^(their maximum - the row's): one CTA per row, a warp for every fourth
+// range. Rows of units in one range are done already; rows of empty sequences are in none and become zero here.
 template <int D>
-__global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ CacheAttnArgs a) {
+__global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ CacheAttnArgs a, int ctas) {
     constexpr int E = D / 32;
     __shared__ float sum[4][D], dens[4];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t id = blockIdx.x;
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = lane_id();
+    const int64_t tok = id / a.heads;
+    const int head = (int)(id - tok * a.heads), seq = (int)(tok / a.tokens), token = (int)(tok - (int64_t)seq * a.tokens);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int64_t unit_pos;
+    const CaWork w = ca_work(a, ctas, seq, unit_pos);
+    int len;
+    const int n_tiles = ca_tiles_of(a, seq, len);
+    if (a.g.lens[seq] != len && threadIdx.x == 0) atomicOr(&g_device_error, kDevErrBadData);
+    const int row = token * a.group + head % a.group;
+    unit_pos += (int64_t)(head / a.group * a.tiles + row / kCaRows) * n_tiles;
+    const int64_t first = unit_pos / w.range;
+    const int splits = n_tiles ? (int)((unit_pos + n_tiles - 1) / w.range - first) + 1 : 0;
+    if (splits == 1) return;
     const float2* const ml = a.part_ml + id * a.splits;
     float top = -INFINITY;
-    for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, ml[s].x);
+    for (int s = lane; s < splits; s += 32) top = fmaxf(top, ml[s].x);
 #pragma unroll
     for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
     float den = 0.0f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
 #pragma unroll 4
-    for (int s = warp; s < a.splits; s += 4) {
+    for (int s = warp; s < splits; s += 4) {
         const float2 p = ml[s];
         const float f = p.x == -INFINITY ? 0.0f : ex2_approx(p.x - top);
         const float* const src = a.part_o + (id * a.splits + s) * D + lane;
@@ -407,8 +509,6 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
     if (lane == 0) dens[warp] = den;
     __syncthreads();
     den = (dens[0] + dens[1]) + (dens[2] + dens[3]);
-    const int64_t tok = id / a.heads;
-    const int head = (int)(id - tok * a.heads), seq = (int)(tok / a.tokens), token = (int)(tok - (int64_t)seq * a.tokens);
     if (threadIdx.x < D / 2) {
         const int d = 2 * threadIdx.x;
         const float inv = top == -INFINITY ? 0.0f : 1.0f / den;
