@@ -134,36 +134,62 @@ def _token_dtype(shape):
     return {DTYPE_F32: "float32", DTYPE_BF16: "bfloat16"}.get(shape.dtype)
 
 
+_torch_module = None
+_dtypes = {}
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _dtypes.update({n: getattr(torch, n) for n in ("float32", "bfloat16", "int32", "float8_e4m3fn")})
+        _torch_module = torch
+    return _torch_module
+
+
 def _ptrs(*specs):
     """Device pointers of arguments given as (value, name, dtype, numel). None stays NULL and an int is taken as a raw
     device pointer (the caller vouches for its size). A tensor must have the expected dtype (if given), hold at least
     `numel` elements (if given), be contiguous and live on the current CUDA device, so that a wrong buffer is refused
-    here instead of being read or written out of bounds. The dtype, size and layout of every argument are checked
-    before any argument's device."""
-    tensors = [(t, name) for t, name, _, _ in specs if t is not None and not isinstance(t, int)]
-    if tensors:
-        import torch
+    here instead of being read or written out of bounds on the GPU. A negative numel -n asks for n dimensions with any
+    strides but a contiguous last one instead. The dtype, size and layout of every argument are checked before any
+    argument's device."""
+    torch = _torch()
+    out, where = [], []
     for t, name, dtype, numel in specs:
         if t is None or isinstance(t, int):
+            out.append(t)
             continue
-        if dtype is not None and t.dtype != getattr(torch, dtype):
+        if dtype is not None and t.dtype is not _dtypes[dtype]:
             raise ValueError(f"{name}: expected torch.{dtype}, got {t.dtype}")
-        if numel is not None and t.numel() < numel:
-            raise ValueError(f"{name}: holds {t.numel()} elements, the shape needs {numel}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous tensor")
-    for t, name in tensors:
-        if not t.is_cuda:
-            raise ValueError(f"{name}: expected a CUDA tensor")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name}: lives on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return tuple(t if (t is None or isinstance(t, int)) else t.data_ptr() for t, _, _, _ in specs)
+        if numel is not None and numel < 0:
+            if t.dim() != -numel:
+                raise ValueError(f"{name}: expected {-numel} dimensions, got {t.dim()}")
+            if t.stride(-1) != 1 and t.shape[-1] > 1:
+                raise ValueError(f"{name}: the last dimension must be contiguous")
+        else:
+            if numel is not None and t.numel() < numel:
+                raise ValueError(f"{name}: holds {t.numel()} elements, the shape needs {numel}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name}: expected a contiguous tensor")
+        where.append(t.get_device())  # -1 on the host
+        out.append(t.data_ptr())
+    if where and min(where) < 0:
+        name = next(s[1] for s in specs if s[0] is not None and not isinstance(s[0], int) and s[0].get_device() < 0)
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if where:
+        here = torch.cuda.current_device()
+        if where.count(here) != len(where):
+            t, name = next(s[:2] for s in specs
+                           if s[0] is not None and not isinstance(s[0], int) and s[0].get_device() != here)
+            raise ValueError(f"{name}: lives on {t.device}, the current device is cuda:{here}")
+    return out
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        torch = _torch()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -280,80 +306,57 @@ def losa_sparse_attn(shape, q, k, v, scale, indptr, kv_block_idx, order, o, lse=
     return _check(st, "losa_sparse_attn", raise_on_error)
 
 
-def _strided(t, name, dtype, ndim):
-    """Device pointer of a tensor that may have any strides but a contiguous last dimension."""
-    import torch
-    if t.dtype != getattr(torch, dtype):
-        raise ValueError(f"{name}: expected torch.{dtype}, got {t.dtype}")
-    if t.dim() != ndim:
-        raise ValueError(f"{name}: expected {ndim} dimensions, got {t.dim()}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr()
-
-
-def _on_device(*specs):
-    import torch
-    here = torch.cuda.current_device() if any(t.is_cuda for t, _ in specs) else None
-    for t, name in specs:
-        if not t.is_cuda:
-            raise ValueError(f"{name}: expected a CUDA tensor")
-        if t.device.index != here:
-            raise ValueError(f"{name}: lives on {t.device}, the current device is cuda:{here}")
-
-
-_NAMES = {"torch.float32": ("float32", DTYPE_F32), "torch.bfloat16": ("bfloat16", DTYPE_BF16)}
-
-
 def _float_dtype(t, name):
-    got = _NAMES.get(str(t.dtype))
-    if got is None:
-        raise ValueError(f"{name}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
-    return got
+    if t.dtype is _torch().bfloat16:
+        return "bfloat16", DTYPE_BF16
+    if t.dtype is _torch().float32:
+        return "float32", DTYPE_F32
+    raise ValueError(f"{name}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
 
 
 def losa_rope_apply(rope, x, y, rotate=1, inverse=False, positions=None, start=None, stream=None, raise_on_error=True):
     """x, y: (parts, batch, tokens, heads, head_dim) views of any layouts (last dimension contiguous); y may hold more
     tokens, which become zero rows. `rotate` is a bit mask of the parts that are rotated."""
     dt, code = _float_dtype(x, "x")
-    px, py = _strided(x, "x", dt, 5), _strided(y, "y", dt, 5)
-    for t, name in ((x, "x"), (y, "y")):
-        if t.shape[4] != rope.head_dim:
-            raise ValueError(f"{name}: rows of {t.shape[4]}, the rotation is for {rope.head_dim}")
-    pp, ps = _ptrs((positions, "positions", "int32", 3 * x.shape[1] * x.shape[2]), (start, "start", "int32", x.shape[1]))
-    _on_device((x, "x"), (y, "y"))
-    xs, ys = x.stride(), y.stride()
-    xv = LosaTokenView(*x.shape[:4], *xs[:4])
-    yv = LosaTokenView(*y.shape[:4], *ys[:4])
+    if x.dim() != 5 or y.dim() != 5 or x.shape[4] != rope.head_dim or y.shape[4] != rope.head_dim:
+        raise ValueError(f"x, y: shapes {tuple(x.shape)}, {tuple(y.shape)}, expected (parts, batch, tokens, heads, "
+                         f"{rope.head_dim})")
+    xn, yn = x.shape, y.shape
+    px, py, pp, ps = _ptrs((x, "x", dt, -5), (y, "y", dt, -5), (positions, "positions", "int32", 3 * xn[1] * xn[2]),
+                           (start, "start", "int32", xn[1]))
+    xv = LosaTokenView(*xn[:4], *x.stride()[:4])
+    yv = LosaTokenView(*yn[:4], *y.stride()[:4])
     st = load().losa_rope_apply(ctypes.byref(rope), code, ctypes.byref(xv), px, ctypes.byref(yv), py, int(rotate),
                                 int(bool(inverse)), pp, ps, _stream(stream))
     return _check(st, "losa_rope_apply", raise_on_error)
 
 
-def _pool_ptrs(cache, k8, v8, k_scale, v_scale, page_table, lens):
+def _pool(cache, k8, v8, k_scale, v_scale, page_table, lens):
+    """_ptrs specs of a cache's buffers."""
     n = max(cache.n_pages, 0) * max(cache.kv_heads, 0)
     codes = n * max(cache.page_tokens, 0) * max(cache.head_dim, 0)
-    return _ptrs((k8, "k8", "float8_e4m3fn", codes), (v8, "v8", "float8_e4m3fn", codes),
-                 (k_scale, "k_scale", "float32", n), (v_scale, "v_scale", "float32", n),
-                 (page_table, "page_table", "int32", max(cache.seqs, 0) * max(cache.table_stride, 0)),
-                 (lens, "lens", "int32", cache.seqs))
+    seqs = max(cache.seqs, 0)
+    return ((k8, "k8", "float8_e4m3fn", codes), (v8, "v8", "float8_e4m3fn", codes),
+            (k_scale, "k_scale", "float32", n), (v_scale, "v_scale", "float32", n),
+            (page_table, "page_table", "int32", seqs * max(cache.table_stride, 0)), (lens, "lens", "int32", seqs))
 
 
 def losa_cache_append(cache, k, v, k8, v8, k_scale, v_scale, page_table, lens, new_tokens, indptr=None, new_lens=None,
                       rope=None, positions=None, stream=None, raise_on_error=True):
     """k, v: (tokens, kv_heads, head_dim) of all sequences' new tokens, strided alike or not."""
     dt, code = _float_dtype(k, "k")
-    pk, pv = _strided(k, "k", dt, 3), _strided(v, "v", dt, 3)
-    for t, name in ((k, "k"), (v, "v")):
-        if tuple(t.shape) != (k.shape[0], cache.kv_heads, cache.head_dim):
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (tokens, {cache.kv_heads}, {cache.head_dim})")
-    p8, pv8, pks, pvs, pt, pl = _pool_ptrs(cache, k8, v8, k_scale, v_scale, page_table, lens)
-    pi, pn, pp = _ptrs((indptr, "indptr", "int32", cache.seqs + 1), (new_lens, "new_lens", "int32", cache.seqs),
-                       (positions, "positions", "int32", 3 * k.shape[0]))
-    _on_device((k, "k"), (v, "v"))
-    st = load().losa_cache_append(ctypes.byref(cache), None if rope is None else ctypes.byref(rope), code, pk,
-                                  k.stride(0), k.stride(1), pv, v.stride(0), v.stride(1), k.shape[0], int(new_tokens),
-                                  pi, pp, pt, pl, pn, p8, pv8, pks, pvs, _stream(stream))
+    n = k.shape[0]
+    if tuple(k.shape) != (n, cache.kv_heads, cache.head_dim) or v.shape != k.shape:
+        raise ValueError(f"k, v: shapes {tuple(k.shape)}, {tuple(v.shape)}, expected (tokens, {cache.kv_heads}, "
+                         f"{cache.head_dim}) of both")
+    p8, pv8, pks, pvs, pt, pl, pk, pv, pi, pn, pp = _ptrs(
+        *_pool(cache, k8, v8, k_scale, v_scale, page_table, lens), (k, "k", dt, -3), (v, "v", dt, -3),
+        (indptr, "indptr", "int32", cache.seqs + 1), (new_lens, "new_lens", "int32", cache.seqs),
+        (positions, "positions", "int32", 3 * n))
+    ks, vs = k.stride(), v.stride()
+    st = load().losa_cache_append(ctypes.byref(cache), None if rope is None else ctypes.byref(rope), code, pk, ks[0], ks[1],
+                                  pv, vs[0], vs[1], n, int(new_tokens), pi, pp, pt, pl, pn, p8, pv8, pks, pvs,
+                                  _stream(stream))
     return _check(st, "losa_cache_append", raise_on_error)
 
 
@@ -365,16 +368,18 @@ def losa_cache_attn(cache, q, k8, v8, k_scale, v_scale, page_table, lens, scale,
                     workspace=None, stream=None, raise_on_error=True):
     """q, o: (seqs, tokens, heads, head_dim) bf16, any strides but a contiguous last dimension; lse: (seqs, tokens,
     heads). max_len bounds the lengths (0: the page table's capacity)."""
-    pq, po = _strided(q, "q", "bfloat16", 4), _strided(o, "o", "bfloat16", 4)
-    if q.shape[0] != cache.seqs or q.shape[3] != cache.head_dim or o.shape != q.shape:
+    if q.dim() != 4:
+        raise ValueError(f"q: expected 4 dimensions, got {q.dim()}")
+    seqs, tokens, heads, d = q.shape
+    if seqs != cache.seqs or d != cache.head_dim or o.shape != q.shape:
         raise ValueError(f"q, o: shapes {tuple(q.shape)}, {tuple(o.shape)}, expected ({cache.seqs}, tokens, heads, "
                          f"{cache.head_dim}) of both")
-    p8, pv8, pks, pvs, pt, pl = _pool_ptrs(cache, k8, v8, k_scale, v_scale, page_table, lens)
-    pe, pw = _ptrs((lse, "lse", "float32", q.shape[0] * q.shape[1] * q.shape[2]), (workspace, "workspace", None, None))
-    _on_device((q, "q"), (o, "o"))
+    p8, pv8, pks, pvs, pt, pl, pq, po, pe, pw = _ptrs(
+        *_pool(cache, k8, v8, k_scale, v_scale, page_table, lens), (q, "q", "bfloat16", -4), (o, "o", "bfloat16", -4),
+        (lse, "lse", "float32", seqs * tokens * heads), (workspace, "workspace", None, None))
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     qs, os_ = q.stride(), o.stride()
-    st = load().losa_cache_attn(ctypes.byref(cache), q.shape[2], q.shape[1], int(bool(causal)), pq, qs[0], qs[1], qs[2],
+    st = load().losa_cache_attn(ctypes.byref(cache), heads, tokens, int(bool(causal)), pq, qs[0], qs[1], qs[2],
                                 pt, pl, p8, pv8, pks, pvs, float(scale), int(max_len), po, os_[0], os_[1], os_[2], pe, pw,
                                 wsb, _stream(stream))
     return _check(st, "losa_cache_attn", raise_on_error)
@@ -384,11 +389,10 @@ def losa_cache_sparse_attn(shape, cache, q, k8, v8, k_scale, v_scale, page_table
                            kv_block_idx=None, order=None, lse=None, stream=None, raise_on_error=True):
     """losa_sparse_attn over the paged 8-bit cache; without lists every block of the sequence is attended to."""
     H, Np, d, nq, _ = _dims(shape)
-    p8, pv8, pks, pvs, pt, pl = _pool_ptrs(cache, k8, v8, k_scale, v_scale, page_table, lens)
-    pq, pi, px, pr, po, pe = _ptrs(
-        (q, "q", "bfloat16", H * Np * d), (indptr, "indptr", "int32", H * nq + 1),
-        (kv_block_idx, "kv_block_idx", "int32", None), (order, "order", "int32", H * nq), (o, "o", "bfloat16", H * Np * d),
-        (lse, "lse", "float32", H * Np))
+    p8, pv8, pks, pvs, pt, pl, pq, pi, px, pr, po, pe = _ptrs(
+        *_pool(cache, k8, v8, k_scale, v_scale, page_table, lens), (q, "q", "bfloat16", H * Np * d),
+        (indptr, "indptr", "int32", H * nq + 1), (kv_block_idx, "kv_block_idx", "int32", None),
+        (order, "order", "int32", H * nq), (o, "o", "bfloat16", H * Np * d), (lse, "lse", "float32", H * Np))
     st = load().losa_cache_sparse_attn(ctypes.byref(shape), ctypes.byref(cache), pq, pt, pl, p8, pv8, pks, pvs,
                                        float(scale), pi, px, pr, po, pe, _stream(stream))
     return _check(st, "losa_cache_sparse_attn", raise_on_error)

@@ -31,8 +31,8 @@ RopeArgs rope_args(const losa_rope* r) {
         const long double ratio = m ? powl((long double)r->theta, -2.0L / m) : 1.0L;
         long double f = inv_two_pi;
         for (int i = 0; i < m / 2; ++i, f *= ratio) {
-            const long double frac = f - floorl(f);
-            const long double fixed = roundl(frac * 18446744073709551616.0L);
+            const long double turns = f < 1.0L ? f : f - floorl(f);  // theta < 1 turns by more than one
+            const long double fixed = turns * 18446744073709551616.0L + 0.5L;
             a.step[at / 2 + i] = fixed >= 18446744073709551616.0L ? 0ull : (uint64_t)fixed;
         }
         at += m;
