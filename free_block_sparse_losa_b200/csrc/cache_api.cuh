@@ -126,10 +126,10 @@ losa_status launch_append_width(int width, const AppendArgs& a, const void* k, c
 
 // Where every sequence is short (max_len), or there is no more than one unit's worth of CTAs to gain, a CTA takes a unit and
 // there is nothing to join: up to 1024 keys the join would cost more than it saves (a warp then has eight tiles). Otherwise
-// two CTAs per SM share all units' keys in equal ranges; a unit, at most 1 / (kv heads x row tiles) of the work, lies in at
+// two or three CTAs per SM share all units' keys in equal ranges; a unit, at most 1 / (kv heads x row tiles) of the work, lies in at
 // most CTAs / (kv heads x row tiles) + 2 of them, and in at most kCaMaxSplits (see ca_work).
 struct AttnPlan {
-    int tiles, splits, ctas;
+    int tile_rows, tiles, splits, ctas;
     int64_t rows;
     size_t ml_bytes, total;
 };
@@ -137,7 +137,8 @@ struct AttnPlan {
 AttnPlan attn_plan(const losa_cache* c, int heads, int tokens, int max_len, int sms) {
     AttnPlan p;
     const int64_t rows = (int64_t)tokens * (heads / c->kv_heads);
-    p.tiles = (int)((rows + kCaRows - 1) / kCaRows);
+    p.tile_rows = rows <= kCaRows<1> ? kCaRows<1> : kCaRows<2>;
+    p.tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
     p.rows = (int64_t)c->seqs * tokens * heads;
     const int64_t units = (int64_t)c->kv_heads * p.tiles;
     const int64_t cap = (int64_t)c->table_stride * c->page_tokens;
@@ -146,7 +147,7 @@ AttnPlan attn_plan(const losa_cache* c, int heads, int tokens, int max_len, int 
     p.splits = 0;
     p.ctas = (int)(units * c->seqs);
     if (len <= 1024 || units * c->seqs > (1 << 20)) return p;
-    p.ctas = 2 * sms;
+    p.ctas = (p.tile_rows == kCaRows<1> ? kCaCtas<1> : kCaCtas<2>) * sms;
     int64_t s = (p.ctas + units - 1) / units + 2;
     if (s > kCaMaxSplits) s = kCaMaxSplits;
     p.splits = (int)s;
@@ -159,15 +160,15 @@ bool attn_shape_ok(const losa_cache* c, int heads, int tokens) {
     return heads > 0 && heads % c->kv_heads == 0 && tokens > 0 && (int64_t)tokens * heads <= (1 << 24);
 }
 
-template <int D>
+template <int D, int NB>
 losa_status launch_cache_attn(const losa_cache* c, CacheAttnArgs& a, const AttnPlan& p, const void* k8, const void* v8,
                               cudaStream_t stream) {
     CUtensorMap tk, tv;
     if (!make_code_map(&tk, c, k8, kCaKeys) || !make_code_map(&tv, c, v8, kCaKeys)) return LOSA_ERR_CUDA;
-    if (cudaFuncSetAttribute(cache_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kCaSmem<D>) != cudaSuccess)
+    if (cudaFuncSetAttribute(cache_attn_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kCaSmem<D, NB>) != cudaSuccess)
         return LOSA_ERR_CUDA;
-    cache_attn_kernel<D><<<p.ctas, kCaWarps * 32, kCaSmem<D>, stream>>>(tk, tv, a);
+    cache_attn_kernel<D, NB><<<p.ctas, kCaWarps * 32, kCaSmem<D, NB>, stream>>>(tk, tv, a);
     const losa_status st = launch_status();
     if (st != LOSA_OK || p.splits == 0) return st;
     // the join may be scheduled while the splits drain; it waits for their results itself
@@ -360,12 +361,16 @@ losa_status losa_cache_attn(const losa_cache* cache, int32_t heads, int32_t toke
     a.tiles = p.tiles;
     a.splits = p.splits;
     a.seqs = cache->seqs;
+    a.tile_rows = p.tile_rows;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.part_ml = static_cast<float2*>(workspace);
     a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.ml_bytes);
     a.wait_limit_ns = g_wait_limit_ns;
-    return cache->head_dim == 128 ? launch_cache_attn<128>(cache, a, p, k8, v8, stream)
-                                  : launch_cache_attn<64>(cache, a, p, k8, v8, stream);
+    if (p.tile_rows == kCaRows<1>)
+        return cache->head_dim == 128 ? launch_cache_attn<128, 1>(cache, a, p, k8, v8, stream)
+                                      : launch_cache_attn<64, 1>(cache, a, p, k8, v8, stream);
+    return cache->head_dim == 128 ? launch_cache_attn<128, 2>(cache, a, p, k8, v8, stream)
+                                  : launch_cache_attn<64, 2>(cache, a, p, k8, v8, stream);
 }
 
 losa_status losa_cache_sparse_attn(const losa_shape* shape, const losa_cache* cache, const void* q,

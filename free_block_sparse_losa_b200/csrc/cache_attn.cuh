@@ -21,9 +21,7 @@
 namespace losa {
 
 constexpr int kCaWarps = 4;
-constexpr int kCaStages = 3;   // tiles in flight per warp
 constexpr int kCaKeys = 32;    // keys of a warp's tile: never more than one page
-constexpr int kCaRows = 16;    // query rows of a CTA
 constexpr int kCaMaxSplits = 128;
 constexpr float kCaBias = 10.0f;
 
@@ -36,7 +34,8 @@ struct CacheAttnArgs {
     float* lse;                // [seqs][tokens][heads] or null
     int64_t q_seq, q_token, q_head, o_seq, o_token, o_head;
     int heads, group, tokens, causal;
-    int tiles;                 // 16-row tiles of a (sequence, kv head)
+    int tiles;                 // row tiles of a (sequence, kv head)
+    int tile_rows;
     int seqs;
     int splits;                // 0: one CTA per unit; else the most CTAs that share a unit
     float scale_log2;
@@ -66,6 +65,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The 8 x 8 matrix of 16-bit elements whose row g lies in lanes 4 g .. 4 g + 3, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
@@ -128,39 +133,51 @@ __device__ __forceinline__ CaWork ca_work(const CacheAttnArgs& a, int ctas, int 
 __device__ __forceinline__ int key_of_column(int n) { return (n & 1) ? ((n - 1) ^ 4) | 1 : n; }
 
 template <int D> constexpr uint32_t kCaTile = kCaKeys * D;  // bytes of a warp's key or value tile
-template <int D> constexpr uint32_t kCaSmem =
-    kCaWarps * kCaStages * 2 * kCaTile<D> + kCaWarps * kCaStages * 16 + kCaWarps * kCaRows * 8 + 1024;
+// NB: 8-row groups of a CTA's row tile. Up to eight rows, half the accumulators and products are enough, and three CTAs
+// (twelve warps) fit on an SM instead of two.
+template <int NB> constexpr int kCaRows = 8 * NB;
+template <int NB> constexpr int kCaStages = NB == 1 ? 2 : 3;  // tiles in flight per warp
+template <int NB> constexpr int kCaCtas = NB == 1 ? 3 : 2;    // per SM
+template <int D, int NB> constexpr uint32_t kCaSmem =
+    kCaWarps * kCaStages<NB> * (2 * kCaTile<D> + 8) + kCaWarps * kCaRows<NB> * 8 + 1024;
 
-// Reads the codes once and does little else, so it is bound by memory. A warp owns a ring of 32-key tiles that TMA fills
-// (one lane issues, one barrier per tile, no exchange between warps until the end): three tiles of 8 KB for each of eight
-// warps keep 190 KB in flight per SM, several times what the latency asks for. S and P V run on mma.m16n8k16 with the
-// query rows as the 16 rows of A: the contraction is two orders of magnitude below the tensor peak here, and operands in
-// registers need no further copy through shared memory, which tcgen05 would.
-template <int D>
-__global__ void __launch_bounds__(kCaWarps * 32, 2)
+// Reads the codes once and does little else: the memory rate bounds it, if enough warps share the latency of the
+// conversions and products in between. A warp owns a ring of 32-key tiles that TMA fills (one lane issues, one barrier per
+// tile, no exchange between warps until the end of a unit). The products are taken transposed, S^T = K Q^T and
+// O^T = V^T P^T on mma.m16n8k16, with the codes as the 16-row operand: 8 query rows then fill the other side, where the
+// usual orientation would leave half of 16 rows empty (92 -> 7x us on eight ragged streams of four rows). P^T comes out of
+// S^T by movmatrix. The contraction is two orders of magnitude below the tensor peak here, and operands in registers need
+// no further copy through shared memory, which tcgen05 would.
+template <int D, int NB>
+__global__ void __launch_bounds__(kCaWarps * 32, kCaCtas<NB>)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CacheAttnArgs a) {
+    constexpr int ROWS = kCaRows<NB>, STAGES = kCaStages<NB>;
     constexpr uint32_t TILE = kCaTile<D>;
     constexpr int HK = D / 64;    // 16-byte pieces of a key row that a lane holds
     constexpr int VW = D / 32;    // 4-byte words of a value row that a lane holds
-    constexpr int NT = D / 8;     // 8-column tiles of O
+    constexpr int MT = D / 16;    // 16-row tiles of O^T
+    constexpr int VD = D / 8;     // dimensions of a value row that a lane holds
     extern __shared__ __align__(1024) uint8_t ca_smem[];
     const uint32_t raw = smem_addr(ca_smem);
     uint8_t* const smem = ca_smem + (((raw + 1023u) & ~1023u) - raw);  // swizzled tiles need 1024-byte alignment
     const uint32_t base = smem_addr(smem);
-    constexpr uint32_t BARS = kCaWarps * kCaStages * 2 * TILE;
+    constexpr uint32_t BARS = kCaWarps * STAGES * 2 * TILE;
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = lane_id();
     const int g = lane >> 2, t = lane & 3;
-    const uint32_t ring = base + warp * kCaStages * 2 * TILE;
-    const uint32_t bar = base + BARS + warp * kCaStages * 8;
-    float2* const tile_scale = reinterpret_cast<float2*>(smem + BARS + kCaWarps * kCaStages * 8) + warp * kCaStages;
-    float2* const row_ml = reinterpret_cast<float2*>(smem + BARS + kCaWarps * kCaStages * 16);
+    const uint32_t ring = base + warp * STAGES * 2 * TILE;
+    const uint32_t bar = base + BARS + warp * STAGES * 8;
+    float2* const row_ml = reinterpret_cast<float2*>(smem + BARS + kCaWarps * STAGES * 8);
 
     const int C = a.g.page;
     const int units = a.g.kv_heads * a.tiles;
+    // the join's CTAs may take the room that these leave one by one: they wait for the whole grid themselves
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (lane == 0) {
-        for (int s = 0; s < kCaStages; ++s) mbar_init(bar + 8 * s, 1);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+        for (int s = 0; s < STAGES; ++s) mbar_init(bar + 8 * s, 1);
         fence_barrier_init();
     }
     __syncwarp();
@@ -215,171 +232,188 @@ __global__ void __launch_bounds__(kCaWarps * 32, 2)
     const int t0 = (int)(pos - unit_pos), t1 = n_tiles == 0 ? 0 : (int)min((int64_t)n_tiles, stop - unit_pos);
     const int mine = max(0, (t1 - t0 - warp + kCaWarps - 1) / kCaWarps);  // this warp's tiles: t0 + warp, + 4, ...
 
-    // Page and scales of the next 32 tiles, one tile per lane; a bad page is reported and its keys do not exist.
-    int at_row = 0;
+    // Page and scales of the next 32 tiles, one tile per lane; a bad page is reported and its keys do not exist. The scales
+    // are first needed when a tile has arrived, so the copies do not wait for them.
+    int at_row = -1, at_page = 0;
     float at_ks = 1.0f, at_vs = 1.0f;
     const uint32_t base_fill = filled;
-    auto issue = [&](int j) {
-        if ((j & 31) == 0) {
-            const int i = j + (int)lane;
-            at_row = -1;
-            at_ks = at_vs = 1.0f;
-            if (i < mine) {
-                const int key = (t0 + warp + i * kCaWarps) * kCaKeys, blk = key / C;
-                const int page = a.g.table[(int64_t)seq * a.g.table_stride + blk];
-                if (page < 0 || page >= a.g.n_pages) {
-                    atomicOr(&g_device_error, kDevErrBadData);
-                } else {
-                    const int64_t ph = (int64_t)page * a.g.kv_heads + kvh;
-                    at_row = (int)(ph * C + (key - blk * C));
-                    at_ks = a.k_scale[ph];
-                    at_vs = fmaxf(a.v_scale[ph], 1e-30f);
-                }
-            }
+    auto pages = [&](int j) {
+        const int i = j + (int)lane;
+        at_row = -1;
+        if (i < mine) {
+            const int key = (t0 + warp + i * kCaWarps) * kCaKeys, blk = key / C;
+            at_page = a.g.table[(int64_t)seq * a.g.table_stride + blk];
+            if (at_page < 0 || at_page >= a.g.n_pages) atomicOr(&g_device_error, kDevErrBadData);
+            else at_row = (int)(((int64_t)at_page * a.g.kv_heads + kvh) * C + (key - blk * C));
         }
+    };
+    auto scales = [&]() {
+        at_ks = at_row < 0 ? -1.0f : a.k_scale[(int64_t)at_page * a.g.kv_heads + kvh];
+        at_vs = at_row < 0 ? 1.0f : fmaxf(a.v_scale[(int64_t)at_page * a.g.kv_heads + kvh], 1e-30f);
+    };
+    auto issue = [&](int j) {
         const int row = __shfl_sync(0xffffffffu, at_row, j & 31);
-        const float ks = __shfl_sync(0xffffffffu, at_ks, j & 31), vs = __shfl_sync(0xffffffffu, at_vs, j & 31);
-        const uint32_t s = (base_fill + j) % kCaStages;
+        const uint32_t s = (base_fill + j) % STAGES;
         if (lane == 0) {
-            tile_scale[s] = make_float2(row < 0 ? -1.0f : ks, vs);
             mbar_arrive_expect_tx(bar + 8 * s, 2 * TILE);
             tma_load_2d(ring + s * 2 * TILE, &tmK, 0, max(row, 0), bar + 8 * s);
             tma_load_2d(ring + s * 2 * TILE + TILE, &tmV, 0, max(row, 0), bar + 8 * s);
         }
         ++filled;
     };
-    for (int j = 0; j < kCaStages && j < mine; ++j) issue(j);
+    pages(0);
+    for (int j = 0; j < STAGES && j < mine; ++j) issue(j);
+    scales();
 
-    // Query rows g and g + 8 of the tile as A fragments: step (h, i) holds dimensions 64 h + 16 t + 4 i .. + 3.
+    // Query rows as B fragments, row 8 nb + g: step (h, i) holds dimensions 64 h + 16 t + 4 i .. + 3. A lane's columns of S^T
+    // and O^T are rows 2 t and 2 t + 1.
     const int n_rows = a.tokens * a.group;
-    uint32_t qa[HK * 4][4];
-    float c[2];
-    int lim[2];
-    {
-        uint32_t amax[2] = {0, 0};
-        uint2 w[2][HK * 4];
+    uint32_t qb[NB][HK * 4][2];
+    float c[NB][2];
+    int lim[NB][2];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int r = tile * kCaRows + g + 8 * half;
-            const int token = r / a.group, head = kvh * a.group + r % a.group;
-            lim[half] = r < n_rows && a.causal ? len - (a.tokens - 1 - token) : len;
-            const __nv_bfloat16* const src = a.q + seq * a.q_seq + token * a.q_token + head * a.q_head + 16 * t;
+    for (int nb = 0; nb < NB; ++nb) {
+        const int r = tile * ROWS + 8 * nb + g;
+        const int token = r / a.group, head = kvh * a.group + r % a.group;
+        const __nv_bfloat16* const src = a.q + seq * a.q_seq + token * a.q_token + head * a.q_head + 16 * t;
+        uint2 w[HK * 4];
+        uint32_t amax = 0;
 #pragma unroll
-            for (int s = 0; s < HK * 4; ++s) {
-                w[half][s] = r < n_rows ? *reinterpret_cast<const uint2*>(src + 64 * (s >> 2) + 4 * (s & 3))
-                                        : make_uint2(0, 0);
+        for (int s = 0; s < HK * 4; ++s) {
+            w[s] = r < n_rows ? *reinterpret_cast<const uint2*>(src + 64 * (s >> 2) + 4 * (s & 3)) : make_uint2(0, 0);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint32_t u = x ? w[half][s].y : w[half][s].x;
-                    const uint32_t lo = (u & 0x7fffu) << 16, hi = u & 0x7fff0000u;
-                    amax[half] = max(amax[half], max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
-                }
-            }
-            amax[half] = max(amax[half], __shfl_xor_sync(0xffffffffu, amax[half], 1));
-            amax[half] = max(amax[half], __shfl_xor_sync(0xffffffffu, amax[half], 2));
-            const float f = row_factor(amax[half]);
-            c[half] = a.scale_log2 / f;
-#pragma unroll
-            for (int s = 0; s < HK * 4; ++s) {
-                const uint32_t u0 = w[half][s].x, u1 = w[half][s].y;
-                qa[s][half] = pack_f16x2(__uint_as_float(u0 << 16) * f, __uint_as_float(u0 & 0xffff0000u) * f);
-                qa[s][2 + half] = pack_f16x2(__uint_as_float(u1 << 16) * f, __uint_as_float(u1 & 0xffff0000u) * f);
+            for (int x = 0; x < 2; ++x) {
+                const uint32_t u = x ? w[s].y : w[s].x;
+                const uint32_t lo = (u & 0x7fffu) << 16, hi = u & 0x7fff0000u;
+                amax = max(amax, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
             }
         }
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const float f = row_factor(amax);
+#pragma unroll
+        for (int s = 0; s < HK * 4; ++s) {
+            qb[nb][s][0] = pack_f16x2(__uint_as_float(w[s].x << 16) * f, __uint_as_float(w[s].x & 0xffff0000u) * f);
+            qb[nb][s][1] = pack_f16x2(__uint_as_float(w[s].y << 16) * f, __uint_as_float(w[s].y & 0xffff0000u) * f);
+        }
+        const float cf = a.scale_log2 / f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            c[nb][x] = __shfl_sync(0xffffffffu, cf, 4 * (2 * t + x));
+            const int rr = tile * ROWS + 8 * nb + 2 * t + x;
+            lim[nb][x] = rr < n_rows && a.causal ? len - (a.tokens - 1 - rr / a.group) : len;
+        }
     }
+    const int least = a.causal ? len - (a.tokens - 1) : len;  // keys that every row sees
 
-    float acc[NT][4];
+    float acc[MT][NB][4];
+    float m[NB][2], l[NB][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        for (int n = 0; n < MT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][nb][i] = 0.0f;
+        m[nb][0] = m[nb][1] = -INFINITY;
+        l[nb][0] = l[nb][1] = 0.0f;
+    }
     const int ka = key_of_column(2 * t), kb = key_of_column(2 * t + 1), kg = key_of_column(g);
 
     bool ok = true;
     int j = 0;
     for (; j < mine; ++j) {
-        const uint32_t f = base_fill + j, s = f % kCaStages;
-        if (!(ok = wait_bounded_warp(bar + 8 * s, (f / kCaStages) & 1u, a.wait_limit_ns))) break;
-        const float2 sc = tile_scale[s];  // written before the arrival this wait has seen
+        const uint32_t f = base_fill + j, s = f % STAGES;
+        if (!(ok = wait_bounded_warp(bar + 8 * s, (f / STAGES) & 1u, a.wait_limit_ns))) break;
+        const float2 sc = make_float2(__shfl_sync(0xffffffffu, at_ks, j & 31), __shfl_sync(0xffffffffu, at_vs, j & 31));
         const uint32_t tk = ring + s * 2 * TILE, tv = tk + TILE;
         const int key0 = (t0 + warp + j * kCaWarps) * kCaKeys;
         const int have = sc.x < 0.0f ? 0 : min(kCaKeys, len - key0);  // keys of this tile that exist
-        float sv[4][4];
+        // S^T: 16 keys x 8 rows at a time; a lane's keys are 16 i + kg and 16 i + 8 + kg
+        float sv[2][NB][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sv[n][i] = 0.0f;
-            const int row = 8 * n + kg;
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) sv[i][nb][x] = 0.0f;
 #pragma unroll
             for (int h = 0; h < HK; ++h) {
-                const uint32_t ch = (uint32_t)(4 * h + t);
-                const uint32_t off = D == 128 ? row * 128u + ((ch ^ (row & 7u)) << 4)
-                                              : row * 64u + ((ch ^ ((row >> 1) & 3u)) << 4);
-                const uint4 w = ld_shared_v4(tk + off);
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                uint32_t u[2][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mma_f16(sv[n], qa[4 * h + i], half2_of_e4m3x2(u[i] & 0xffffu), half2_of_e4m3x2(u[i] >> 16));
+                for (int y = 0; y < 2; ++y) {
+                    const uint32_t row = 16 * i + 8 * y + kg, ch = 4 * h + t;
+                    const uint4 w = ld_shared_v4(tk + (D == 128 ? row * 128u + ((ch ^ (row & 7u)) << 4)
+                                                               : row * 64u + ((ch ^ ((row >> 1) & 3u)) << 4)));
+                    u[y][0] = w.x, u[y][1] = w.y, u[y][2] = w.z, u[y][3] = w.w;
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t ka4[4] = {half2_of_e4m3x2(u[0][x] & 0xffffu), half2_of_e4m3x2(u[1][x] & 0xffffu),
+                                             half2_of_e4m3x2(u[0][x] >> 16), half2_of_e4m3x2(u[1][x] >> 16)};
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+                        mma_f16(sv[i][nb], ka4, qb[nb][4 * h + x][0], qb[nb][4 * h + x][1]);
+                }
             }
         }
         // x = t + log2 vs; keys a row does not see become -inf whatever their codes hold
         const float lv = __log2f(sc.y), inv_vs = 1.0f / sc.y;
-        const float ck[2] = {c[0] * sc.x, c[1] * sc.x};
-        const bool whole = have == kCaKeys && key0 + kCaKeys <= min(lim[0], lim[1]);
-        float mx[2] = {-INFINITY, -INFINITY};
+        const bool whole = have == kCaKeys && key0 + kCaKeys <= least;
+        uint32_t pb[2][NB][2];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int nb = 0; nb < NB; ++nb) {
+            float mx[2] = {-INFINITY, -INFINITY};
+            const float ck[2] = {c[nb][0] * sc.x, c[nb][1] * sc.x};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int half = i >> 1, key = 8 * n + ((i & 1) ? kb : ka);
-                float x = fmaf(sv[n][i], ck[half], lv);
-                if (!whole && (key >= have || key0 + key >= lim[half])) x = -INFINITY;
-                sv[n][i] = x;
-                mx[half] = fmaxf(mx[half], x);
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int key = 16 * i + 8 * (x >> 1) + kg;
+                    float v = fmaf(sv[i][nb][x], ck[x & 1], lv);
+                    if (!whole && (key >= have || key0 + key >= lim[nb][x & 1])) v = -INFINITY;
+                    sv[i][nb][x] = v;
+                    mx[x & 1] = fmaxf(mx[x & 1], v);
+                }
+            float ref[2], alpha[2], add[2] = {0.0f, 0.0f};
+            bool moved = false;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (int y = 4; y < 32; y <<= 1) mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], y));
+                const float top = fmaxf(m[nb][x], mx[x]);
+                moved |= top > m[nb][x];
+                alpha[x] = m[nb][x] == -INFINITY ? 0.0f : ex2_approx(m[nb][x] - top);
+                m[nb][x] = top;
+                ref[x] = top == -INFINITY ? 0.0f : kCaBias - top;
             }
-        float ref[2], alpha[2];
-        bool moved = false;
+            if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 1));
-            mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 2));
-            const float top = fmaxf(m[half], mx[half]);
-            moved |= top > m[half];
-            alpha[half] = m[half] == -INFINITY ? 0.0f : ex2_approx(m[half] - top);
-            m[half] = top;
-            ref[half] = top == -INFINITY ? 0.0f : kCaBias - top;
-        }
-        if (__any_sync(0xffffffffu, moved)) {
+                for (int x = 0; x < 2; ++x) l[nb][x] *= alpha[x];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) l[half] *= alpha[half];
+                for (int n = 0; n < MT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[n][i] *= alpha[i >> 1];
-        }
-        uint32_t pa[2][4];
-        float add[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            float p[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p[i] = ex2_approx(sv[n][i] + ref[i >> 1]);
-                add[i >> 1] += p[i];
+                    for (int x = 0; x < 4; ++x) acc[n][nb][x] *= alpha[x & 1];
             }
-            pa[n >> 1][2 * (n & 1)] = pack_f16x2(p[0], p[1]);
-            pa[n >> 1][2 * (n & 1) + 1] = pack_f16x2(p[2], p[3]);
-        }
-        l[0] = fmaf(add[0], inv_vs, l[0]);
-        l[1] = fmaf(add[1], inv_vs, l[1]);
-        // O += P V: value rows of keys that do not exist count as zero whatever they hold
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const float p0 = ex2_approx(sv[i][nb][2 * y] + ref[0]), p1 = ex2_approx(sv[i][nb][2 * y + 1] + ref[1]);
+                    add[0] += p0;
+                    add[1] += p1;
+                    pb[i][nb][y] = transpose8x8(pack_f16x2(p0, p1));
+                }
+            l[nb][0] = fmaf(add[0], inv_vs, l[nb][0]);
+            l[nb][1] = fmaf(add[1], inv_vs, l[nb][1]);
+        }
+        // O^T += V^T P^T: row g of 16-row tile n is dimension VD g + 2 n, row g + 8 the next. Value rows of keys that do not
+        // exist count as zero whatever they hold.
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
             uint32_t u[4][VW];
 #pragma unroll
             for (int r4 = 0; r4 < 4; ++r4) {
-                const int row = 16 * kk + 8 * (r4 >> 1) + ((r4 & 1) ? kb : ka);
+                const uint32_t row = 16 * i + 8 * (r4 >> 1) + ((r4 & 1) ? kb : ka);
                 if (D == 128) {
                     const uint4 w = ld_shared_v4(tv + row * 128u + (((uint32_t)g ^ (row & 7u)) << 4));
                     u[r4][0] = w.x, u[r4][1] = w.y, u[r4][VW - 2] = w.z, u[r4][VW - 1] = w.w;
@@ -388,56 +422,64 @@ __global__ void __launch_bounds__(kCaWarps * 32, 2)
                                                  8u * (g & 1));
                     u[r4][0] = w.x, u[r4][1] = w.y;
                 }
-                if (have < kCaKeys && row >= have) {
+                if (have < kCaKeys && (int)row >= have) {
 #pragma unroll
                     for (int x = 0; x < VW; ++x) u[r4][x] = 0;
                 }
             }
 #pragma unroll
-            for (int x = 0; x < VW; ++x) {
-                const uint32_t ab0 = __byte_perm(u[0][x], u[1][x], 0x5140), ab1 = __byte_perm(u[0][x], u[1][x], 0x7362);
-                const uint32_t cd0 = __byte_perm(u[2][x], u[3][x], 0x5140), cd1 = __byte_perm(u[2][x], u[3][x], 0x7362);
-                mma_f16(acc[4 * x], pa[kk], half2_of_e4m3x2(ab0 & 0xffffu), half2_of_e4m3x2(cd0 & 0xffffu));
-                mma_f16(acc[4 * x + 1], pa[kk], half2_of_e4m3x2(ab0 >> 16), half2_of_e4m3x2(cd0 >> 16));
-                mma_f16(acc[4 * x + 2], pa[kk], half2_of_e4m3x2(ab1 & 0xffffu), half2_of_e4m3x2(cd1 & 0xffffu));
-                mma_f16(acc[4 * x + 3], pa[kk], half2_of_e4m3x2(ab1 >> 16), half2_of_e4m3x2(cd1 >> 16));
-            }
+            for (int x = 0; x < VW; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const uint32_t ab = __byte_perm(u[0][x], u[1][x], y ? 0x7362 : 0x5140);
+                    const uint32_t cd = __byte_perm(u[2][x], u[3][x], y ? 0x7362 : 0x5140);
+                    const uint32_t va[4] = {half2_of_e4m3x2(ab & 0xffffu), half2_of_e4m3x2(ab >> 16),
+                                            half2_of_e4m3x2(cd & 0xffffu), half2_of_e4m3x2(cd >> 16)};
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) mma_f16(acc[2 * x + y][nb], va, pb[i][nb][0], pb[i][nb][1]);
+                }
         }
         __syncwarp();  // every lane has read the tile
-        if (j + kCaStages < mine) issue(j + kCaStages);
+        if (j + STAGES < mine) {
+            // the last tile of the 32 is consumed STAGES tiles after it was issued: pages run ahead of the scales
+            if (((j + STAGES) & 31) == 0) pages(j + STAGES);
+            issue(j + STAGES);
+        }
+        if (((j + 1) & 31) == 0) scales();
     }
     if (!ok)  // copies in flight land before the ring is used for anything else
         for (uint32_t x = base_fill + j; x != filled; ++x)
-            wait_bounded_warp(bar + 8 * (x % kCaStages), (x / kCaStages) & 1u, kDrainLimitNs);
+            wait_bounded_warp(bar + 8 * (x % STAGES), (x / STAGES) & 1u, kDrainLimitNs);
 
-    // Join the four warps through their own rings: [16 rows][D] fp32 each.
+    // Join the four warps through their own rings: [ROWS][D] fp32 each.
+    float* const mine_o = reinterpret_cast<float*>(smem + warp * STAGES * 2 * TILE);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
-        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
-        if (t == 0) row_ml[warp * kCaRows + g + 8 * half] = make_float2(m[half], l[half]);
-    }
-    float* const mine_o = reinterpret_cast<float*>(smem + warp * kCaStages * 2 * TILE);
-    // column 2t (+1) of O tile n is dimension (D / 8) (2t (+1)) + n
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int x = 0; x < 2; ++x) {
+            const int r = 8 * nb + 2 * t + x;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mine_o[(g + 8 * (i >> 1)) * D + NT * (2 * t + (i & 1)) + n] = acc[n][i];
+            for (int y = 4; y < 32; y <<= 1) l[nb][x] += __shfl_xor_sync(0xffffffffu, l[nb][x], y);
+            if (g == 0) row_ml[warp * ROWS + r] = make_float2(m[nb][x], l[nb][x]);
+#pragma unroll
+            for (int n = 0; n < MT; ++n)
+                *reinterpret_cast<float2*>(mine_o + r * D + VD * g + 2 * n) = make_float2(acc[n][nb][x], acc[n][nb][2 + x]);
+        }
     __syncthreads();
     const bool shared = a.splits != 0 && t1 - t0 < n_tiles;  // other CTAs hold the rest of the unit
-    for (int i = threadIdx.x; i < kCaRows * (D / 4); i += kCaWarps * 32) {
+    for (int i = threadIdx.x; i < ROWS * (D / 4); i += kCaWarps * 32) {
         const int r = i / (D / 4), d0 = (i - r * (D / 4)) * 4;
-        const int row = tile * kCaRows + r;
+        const int row = tile * ROWS + r;
         if (row >= n_rows) continue;
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kCaWarps; ++w) top = fmaxf(top, row_ml[w * kCaRows + r].x);
+        for (int w = 0; w < kCaWarps; ++w) top = fmaxf(top, row_ml[w * ROWS + r].x);
         float den = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int w = 0; w < kCaWarps; ++w) {
-            const float2 ml = row_ml[w * kCaRows + r];
+            const float2 ml = row_ml[w * ROWS + r];
             const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - top);
-            const float4 v = *reinterpret_cast<const float4*>(smem + w * kCaStages * 2 * TILE + (r * D + d0) * 4);
+            const float4 v = *reinterpret_cast<const float4*>(smem + w * STAGES * 2 * TILE + (r * D + d0) * 4);
             den = fmaf(ml.y, f, den);
             o[0] = fmaf(v.x, f, o[0]);
             o[1] = fmaf(v.y, f, o[1]);
@@ -462,7 +504,6 @@ __global__ void __launch_bounds__(kCaWarps * 32, 2)
     if (!__syncthreads_and(ok)) break;  // the rings are free again; after a timeout every warp stops
     fence_proxy_async_smem();
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Joins the ranges that share a unit, weighted by 2^(their maximum - the row's): one CTA per row, a warp for every fourth
@@ -483,7 +524,7 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
     const int n_tiles = ca_tiles_of(a, seq, len);
     if (a.g.lens[seq] != len && threadIdx.x == 0) atomicOr(&g_device_error, kDevErrBadData);
     const int row = token * a.group + head % a.group;
-    unit_pos += (int64_t)(head / a.group * a.tiles + row / kCaRows) * n_tiles;
+    unit_pos += (int64_t)(head / a.group * a.tiles + row / a.tile_rows) * n_tiles;
     const int64_t first = unit_pos / w.range;
     const int splits = n_tiles ? (int)((unit_pos + n_tiles - 1) / w.range - first) + 1 : 0;
     if (splits == 1) return;
