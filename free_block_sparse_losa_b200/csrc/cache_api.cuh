@@ -126,7 +126,7 @@ losa_status launch_append_width(int width, const AppendArgs& a, const void* k, c
 
 // Where every sequence is short (max_len), or there is no more than one unit's worth of CTAs to gain, a CTA takes a unit and
 // there is nothing to join: up to 1024 keys the join would cost more than it saves (a warp then has eight tiles). Otherwise
-// two or three CTAs per SM share all units' keys in equal ranges; a unit, at most 1 / (kv heads x row tiles) of the work, lies in at
+// two CTAs per SM share all units' keys in equal ranges; a unit, at most 1 / (kv heads x row tiles) of the work, lies in at
 // most CTAs / (kv heads x row tiles) + 2 of them, and in at most kCaMaxSplits (see ca_work).
 struct AttnPlan {
     int tile_rows, tiles, splits, ctas;
@@ -147,7 +147,7 @@ AttnPlan attn_plan(const losa_cache* c, int heads, int tokens, int max_len, int 
     p.splits = 0;
     p.ctas = (int)(units * c->seqs);
     if (len <= 1024 || units * c->seqs > (1 << 20)) return p;
-    p.ctas = (p.tile_rows == kCaRows<1> ? kCaCtas<1> : kCaCtas<2>) * sms;
+    p.ctas = kCaCtas * sms;
     int64_t s = (p.ctas + units - 1) / units + 2;
     if (s > kCaMaxSplits) s = kCaMaxSplits;
     p.splits = (int)s;

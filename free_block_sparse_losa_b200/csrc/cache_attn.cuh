@@ -100,6 +100,11 @@ __device__ __forceinline__ int ca_tiles_of(const CacheAttnArgs& a, int seq, int&
     return (len + kCaKeys - 1) / kCaKeys;
 }
 
+// A quotient of non-negative numbers; in 32 bits where they fit, which saves about half a microsecond each.
+__device__ __forceinline__ int64_t ca_div(int64_t x, int64_t y) {
+    return (x | y) >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
+}
+
 // Total and range; with seq >= 0 also the tiles before that sequence. Called by a whole warp.
 __device__ __forceinline__ CaWork ca_work(const CacheAttnArgs& a, int ctas, int seq, int64_t& before) {
     const int units = a.g.kv_heads * a.tiles;
@@ -121,10 +126,10 @@ __device__ __forceinline__ CaWork ca_work(const CacheAttnArgs& a, int ctas, int 
     before = head * units;
     CaWork w;
     w.total = sum * units;
-    w.range = (w.total + ctas - 1) / ctas;
+    w.range = ca_div(w.total + ctas - 1, ctas);
     // at least eight tiles for each warp pair of loads to pay, and no unit in more than `splits` ranges
-    const int64_t least = a.splits > 2 ? ((int64_t)most + a.splits - 3) / (a.splits - 2) : most;
-    w.range = max(max(w.range, least), (int64_t)(2 * kCaWarps));
+    const int least = (most + a.splits - 3) / (a.splits - 2);  // splits > 2
+    w.range = max(w.range, (int64_t)max(least, 2 * kCaWarps));
     return w;
 }
 
@@ -133,26 +138,28 @@ __device__ __forceinline__ CaWork ca_work(const CacheAttnArgs& a, int ctas, int 
 __device__ __forceinline__ int key_of_column(int n) { return (n & 1) ? ((n - 1) ^ 4) | 1 : n; }
 
 template <int D> constexpr uint32_t kCaTile = kCaKeys * D;  // bytes of a warp's key or value tile
-// NB: 8-row groups of a CTA's row tile. Up to eight rows, half the accumulators and products are enough, and three CTAs
-// (twelve warps) fit on an SM instead of two.
+// NB: 8-row groups of a CTA's row tile. Up to eight rows, half the accumulators and products are enough.
 template <int NB> constexpr int kCaRows = 8 * NB;
-template <int NB> constexpr int kCaStages = NB == 1 ? 2 : 3;  // tiles in flight per warp
-template <int NB> constexpr int kCaCtas = NB == 1 ? 3 : 2;    // per SM
+// Tiles in flight per warp and CTAs per SM: 128 KB on their way to an SM. More (three tiles, or three CTAs, which eight
+// rows have room for) queue in the memory system and let some SMs finish well before others: 84..86 against 80 us on eight
+// ragged streams of four rows, 95 against 92 us on two long ones of twelve.
+constexpr int kCaStages = 2;
+constexpr int kCaCtas = 2;
 template <int D, int NB> constexpr uint32_t kCaSmem =
-    kCaWarps * kCaStages<NB> * (2 * kCaTile<D> + 8) + kCaWarps * kCaRows<NB> * 8 + 1024;
+    kCaWarps * kCaStages * (2 * kCaTile<D> + 8) + kCaWarps * kCaRows<NB> * 8 + 1024;
 
 // Reads the codes once and does little else: the memory rate bounds it, if enough warps share the latency of the
 // conversions and products in between. A warp owns a ring of 32-key tiles that TMA fills (one lane issues, one barrier per
 // tile, no exchange between warps until the end of a unit). The products are taken transposed, S^T = K Q^T and
 // O^T = V^T P^T on mma.m16n8k16, with the codes as the 16-row operand: 8 query rows then fill the other side, where the
-// usual orientation would leave half of 16 rows empty (92 -> 7x us on eight ragged streams of four rows). P^T comes out of
+// usual orientation would leave half of 16 rows empty (92 against 87 us on eight ragged streams of four rows). P^T comes out of
 // S^T by movmatrix. The contraction is two orders of magnitude below the tensor peak here, and operands in registers need
 // no further copy through shared memory, which tcgen05 would.
 template <int D, int NB>
-__global__ void __launch_bounds__(kCaWarps * 32, kCaCtas<NB>)
+__global__ void __launch_bounds__(kCaWarps * 32, kCaCtas)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CacheAttnArgs a) {
-    constexpr int ROWS = kCaRows<NB>, STAGES = kCaStages<NB>;
+    constexpr int ROWS = kCaRows<NB>, STAGES = kCaStages;
     constexpr uint32_t TILE = kCaTile<D>;
     constexpr int HK = D / 64;    // 16-byte pieces of a key row that a lane holds
     constexpr int VW = D / 32;    // 4-byte words of a value row that a lane holds
@@ -226,14 +233,27 @@ __global__ void __launch_bounds__(kCaWarps * 32, kCaCtas<NB>)
         seq_pos += (int64_t)n_tiles * units;
         n_tiles = ca_tiles_of(a, ++seq, len);
     }
-    const int unit = n_tiles == 0 ? (int)(blockIdx.x % units) : (int)((pos - seq_pos) / n_tiles);
+    const int unit = n_tiles == 0 ? (int)(blockIdx.x % units) : (int)ca_div(pos - seq_pos, n_tiles);
     const int tile = unit % a.tiles, kvh = unit / a.tiles;
     const int64_t unit_pos = seq_pos + (int64_t)unit * n_tiles;
     const int t0 = (int)(pos - unit_pos), t1 = n_tiles == 0 ? 0 : (int)min((int64_t)n_tiles, stop - unit_pos);
     const int mine = max(0, (t1 - t0 - warp + kCaWarps - 1) / kCaWarps);  // this warp's tiles: t0 + warp, + 4, ...
 
+    // Raw query rows, row 8 nb + g of the tile: asked for before the copies of codes, which would hold them up.
+    const int n_rows = a.tokens * a.group;
+    uint2 qw[NB][HK * 4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int r = tile * ROWS + 8 * nb + g;
+        const int token = r / a.group, head = kvh * a.group + r % a.group;
+        const __nv_bfloat16* const src = a.q + seq * a.q_seq + token * a.q_token + head * a.q_head + 16 * t;
+#pragma unroll
+        for (int s = 0; s < HK * 4; ++s)
+            qw[nb][s] = r < n_rows ? *reinterpret_cast<const uint2*>(src + 64 * (s >> 2) + 4 * (s & 3)) : make_uint2(0, 0);
+    }
+
     // Page and scales of the next 32 tiles, one tile per lane; a bad page is reported and its keys do not exist. The scales
-    // are first needed when a tile has arrived, so the copies do not wait for them.
+    // are first needed when a tile has arrived: the copies do not wait for them, but follow them.
     int at_row = -1, at_page = 0;
     float at_ks = 1.0f, at_vs = 1.0f;
     const uint32_t base_fill = filled;
@@ -249,7 +269,7 @@ __global__ void __launch_bounds__(kCaWarps * 32, kCaCtas<NB>)
     };
     auto scales = [&]() {
         at_ks = at_row < 0 ? -1.0f : a.k_scale[(int64_t)at_page * a.g.kv_heads + kvh];
-        at_vs = at_row < 0 ? 1.0f : fmaxf(a.v_scale[(int64_t)at_page * a.g.kv_heads + kvh], 1e-30f);
+        at_vs = at_row < 0 ? 1.0f : a.v_scale[(int64_t)at_page * a.g.kv_heads + kvh];
     };
     auto issue = [&](int j) {
         const int row = __shfl_sync(0xffffffffu, at_row, j & 31);
@@ -262,25 +282,20 @@ __global__ void __launch_bounds__(kCaWarps * 32, kCaCtas<NB>)
         ++filled;
     };
     pages(0);
-    for (int j = 0; j < STAGES && j < mine; ++j) issue(j);
     scales();
+    for (int j = 0; j < STAGES && j < mine; ++j) issue(j);
 
     // Query rows as B fragments, row 8 nb + g: step (h, i) holds dimensions 64 h + 16 t + 4 i .. + 3. A lane's columns of S^T
     // and O^T are rows 2 t and 2 t + 1.
-    const int n_rows = a.tokens * a.group;
     uint32_t qb[NB][HK * 4][2];
     float c[NB][2];
     int lim[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-        const int r = tile * ROWS + 8 * nb + g;
-        const int token = r / a.group, head = kvh * a.group + r % a.group;
-        const __nv_bfloat16* const src = a.q + seq * a.q_seq + token * a.q_token + head * a.q_head + 16 * t;
-        uint2 w[HK * 4];
+        const uint2 (&w)[HK * 4] = qw[nb];
         uint32_t amax = 0;
 #pragma unroll
         for (int s = 0; s < HK * 4; ++s) {
-            w[s] = r < n_rows ? *reinterpret_cast<const uint2*>(src + 64 * (s >> 2) + 4 * (s & 3)) : make_uint2(0, 0);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const uint32_t u = x ? w[s].y : w[s].x;
@@ -324,37 +339,40 @@ __global__ void __launch_bounds__(kCaWarps * 32, kCaCtas<NB>)
     for (; j < mine; ++j) {
         const uint32_t f = base_fill + j, s = f % STAGES;
         if (!(ok = wait_bounded_warp(bar + 8 * s, (f / STAGES) & 1u, a.wait_limit_ns))) break;
-        const float2 sc = make_float2(__shfl_sync(0xffffffffu, at_ks, j & 31), __shfl_sync(0xffffffffu, at_vs, j & 31));
+        const float2 sc = make_float2(__shfl_sync(0xffffffffu, at_ks, j & 31),
+                                      fmaxf(__shfl_sync(0xffffffffu, at_vs, j & 31), 1e-30f));
         const uint32_t tk = ring + s * 2 * TILE, tv = tk + TILE;
         const int key0 = (t0 + warp + j * kCaWarps) * kCaKeys;
         const int have = sc.x < 0.0f ? 0 : min(kCaKeys, len - key0);  // keys of this tile that exist
         // S^T: 16 keys x 8 rows at a time; a lane's keys are 16 i + kg and 16 i + 8 + kg
         float sv[2][NB][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) sv[i][nb][x] = 0.0f;
 #pragma unroll
-            for (int h = 0; h < HK; ++h) {
-                uint32_t u[2][4];
+        for (int h = 0; h < HK; ++h) {
+            uint32_t u[4][4];
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const uint32_t row = 16 * i + 8 * y + kg, ch = 4 * h + t;
-                    const uint4 w = ld_shared_v4(tk + (D == 128 ? row * 128u + ((ch ^ (row & 7u)) << 4)
-                                                               : row * 64u + ((ch ^ ((row >> 1) & 3u)) << 4)));
-                    u[y][0] = w.x, u[y][1] = w.y, u[y][2] = w.z, u[y][3] = w.w;
-                }
+            for (int y = 0; y < 4; ++y) {
+                const uint32_t row = 8 * y + kg, ch = 4 * h + t;
+                const uint4 w = ld_shared_v4(tk + (D == 128 ? row * 128u + ((ch ^ (row & 7u)) << 4)
+                                                           : row * 64u + ((ch ^ ((row >> 1) & 3u)) << 4)));
+                u[y][0] = w.x, u[y][1] = w.y, u[y][2] = w.z, u[y][3] = w.w;
+            }
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const uint32_t ka4[4] = {half2_of_e4m3x2(u[0][x] & 0xffffu), half2_of_e4m3x2(u[1][x] & 0xffffu),
-                                             half2_of_e4m3x2(u[0][x] >> 16), half2_of_e4m3x2(u[1][x] >> 16)};
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t ka4[4] = {
+                        half2_of_e4m3x2(u[2 * i][x] & 0xffffu), half2_of_e4m3x2(u[2 * i + 1][x] & 0xffffu),
+                        half2_of_e4m3x2(u[2 * i][x] >> 16), half2_of_e4m3x2(u[2 * i + 1][x] >> 16)};
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
                         mma_f16(sv[i][nb], ka4, qb[nb][4 * h + x][0], qb[nb][4 * h + x][1]);
                 }
-            }
         }
         // x = t + log2 vs; keys a row does not see become -inf whatever their codes hold
         const float lv = __log2f(sc.y), inv_vs = 1.0f / sc.y;
@@ -489,7 +507,7 @@ __global__ void __launch_bounds__(kCaWarps * 32, kCaCtas<NB>)
         const int token = row / a.group, head = kvh * a.group + row % a.group;
         const int64_t id = ((int64_t)seq * a.tokens + token) * a.heads + head;
         if (shared) {
-            const int64_t at = id * a.splits + (int)(blockIdx.x - unit_pos / range);
+            const int64_t at = id * a.splits + (int)(blockIdx.x - ca_div(unit_pos, range));
             *reinterpret_cast<float4*>(a.part_o + at * D + d0) = make_float4(o[0], o[1], o[2], o[3]);
             if (d0 == 0) a.part_ml[at] = make_float2(top, den);
         } else {
@@ -517,7 +535,7 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
     const uint32_t lane = lane_id();
     const int64_t tok = id / a.heads;
     const int head = (int)(id - tok * a.heads), seq = (int)(tok / a.tokens), token = (int)(tok - (int64_t)seq * a.tokens);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // lens was there before the grid this one follows began: only its results have to be waited for
     int64_t unit_pos;
     const CaWork w = ca_work(a, ctas, seq, unit_pos);
     int len;
@@ -525,9 +543,10 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
     if (a.g.lens[seq] != len && threadIdx.x == 0) atomicOr(&g_device_error, kDevErrBadData);
     const int row = token * a.group + head % a.group;
     unit_pos += (int64_t)(head / a.group * a.tiles + row / a.tile_rows) * n_tiles;
-    const int64_t first = unit_pos / w.range;
-    const int splits = n_tiles ? (int)((unit_pos + n_tiles - 1) / w.range - first) + 1 : 0;
+    const int splits =
+        n_tiles ? (int)(ca_div(unit_pos + n_tiles - 1, w.range) - ca_div(unit_pos, w.range)) + 1 : 0;
     if (splits == 1) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const float2* const ml = a.part_ml + id * a.splits;
     float top = -INFINITY;
     for (int s = lane; s < splits; s += 32) top = fmaxf(top, ml[s].x);
