@@ -46,6 +46,15 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// Four values as codes, the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
 __device__ __forceinline__ uint32_t e4m3x2_of_half2(uint32_t h) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
@@ -125,87 +134,106 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, const T* __rest
     const int h0 = blockIdx.y * a.heads_per_cta, h1 = min(a.g.kv_heads, h0 + a.heads_per_cta);
     const int warps = blockDim.x >> 5;
 
-    // this thread's units: slot and dimensions of each side (slot < 0: none)
-    int slot[P];
-    int dim[P][SIDES];
-    bool turned[P];
-    float2 cs[P][PAIRS];
-    Pack<T, LN> next[P][SIDES][LOADS];
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const int unit = p * (int)blockDim.x + (int)threadIdx.x, row = unit / UNITS, u = unit - row * UNITS;
-        slot[p] = lo + row < hi ? lo + row : -1;
-        dim[p][0] = u * N * SIDES;
-        int pair = dim[p][0];
-        if constexpr (W > 0) {
-            dim[p][1] = dim[p][0] + N;
-            const RopeUnit x = rope_unit<W>(a.r, D, u);  // W > 0 only with a rotation
-            dim[p][0] = x.first;
-            dim[p][1] = x.second;
-            pair = x.pair;
-        }
-        turned[p] = rotate && pair < a.r.end[2];
-#pragma unroll
-        for (int s = 0; s < SIDES; ++s)
-#pragma unroll
-            for (int j = 0; j < LOADS; ++j)
-                if (slot[p] >= 0) next[p][s][j].load(src + (src0 + slot[p]) * ts + h0 * hs + dim[p][s] + j * LN);
-        if (turned[p] && slot[p] >= 0) {
-            const int32_t* triple = a.positions ? a.positions + 3 * (src0 + slot[p]) : nullptr;
-            const RopePos q = rope_position(a.r, triple, blk * C + slot[p]);
-#pragma unroll
-            for (int e = 0; e < PAIRS; ++e) cs[p][e] = rope_pair(a.r, q, pair + 2 * e);
-        }
+    // This thread's units: the same unit u of rows row, row + rows_pass, ... (the block's size is a multiple of UNITS).
+    const int rows_pass = (int)blockDim.x / UNITS, row = (int)threadIdx.x / UNITS, u = (int)threadIdx.x - row * UNITS;
+    int dim0 = u * N * SIDES, dim1 = dim0 + N, pair = dim0;
+    if constexpr (W > 0) {  // only with a rotation
+        const RopeUnit x = rope_unit<W>(a.r, D, u);
+        dim0 = x.first;
+        dim1 = x.second;
+        pair = x.pair;
     }
+    const bool turned = rotate && pair < a.r.end[2];
+    const bool part_turned = turned && pair + 2 * PAIRS > a.r.end[2];  // an interleaved unit's last pairs may stay
+    bool real[P];
+    float2 cs[P][PAIRS];
+    Pack<T, LN> next[P][SIDES][LOADS] = {};  // zeros where there is no row
+    const T* from = src + (src0 + lo + row) * ts + h0 * hs + dim0;
+    const int64_t step = rows_pass * ts;
+    auto fetch = [&]() {
+        const T* x = from;
+#pragma unroll
+        for (int p = 0; p < P; ++p, x += step)
+            if (real[p]) {
+#pragma unroll
+                for (int j = 0; j < LOADS; ++j) {
+                    next[p][0][j].load(x + j * LN);
+                    if (SIDES == 2) next[p][SIDES - 1][j].load(x + (dim1 - dim0) + j * LN);
+                }
+            }
+        from += hs;
+    };
+#pragma unroll
+    for (int p = 0; p < P; ++p) real[p] = lo + row + p * rows_pass < hi;
+    fetch();
+    if (turned) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            if (real[p]) {
+                const int slot = lo + row + p * rows_pass;
+                const int32_t* triple = a.positions ? a.positions + 3 * (src0 + slot) : nullptr;
+                const RopePos q = rope_position(a.r, triple, blk * C + slot);
+#pragma unroll
+                for (int e = 0; e < PAIRS; ++e) cs[p][e] = rope_pair(a.r, q, pair + 2 * e);
+            }
+    }
+    uint8_t* to = code + ((int64_t)page * a.g.kv_heads + h0) * C * D + (lo + row) * D + dim0;
 
+    const int lane = threadIdx.x & 31;
     for (int h = h0; h < h1; ++h) {
         float f[P][SIDES][N];
-        uint32_t amax = 0;
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
             for (int s = 0; s < SIDES; ++s)
 #pragma unroll
-                for (int e = 0; e < N; ++e) f[p][s][e] = slot[p] >= 0 ? next[p][s][e / LN].get(e % LN) : 0.0f;
-        if (h + 1 < h1) {
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-#pragma unroll
-                for (int s = 0; s < SIDES; ++s)
-#pragma unroll
-                    for (int j = 0; j < LOADS; ++j)
-                        if (slot[p] >= 0)
-                            next[p][s][j].load(src + (src0 + slot[p]) * ts + (h + 1) * hs + dim[p][s] + j * LN);
-        }
+                for (int e = 0; e < N; ++e) f[p][s][e] = next[p][s][e / LN].get(e % LN);
+        if (h + 1 < h1) fetch();
+        float top = 0.0f;  // NaN is passed over
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            if (turned[p]) {
+            if (turned) {
 #pragma unroll
                 for (int e = 0; e < PAIRS; ++e) {
                     float& z0 = f[p][0][W ? e : 2 * e];
                     float& z1 = f[p][SIDES - 1][W ? e : 2 * e + 1];
                     const float x0 = z0, x1 = z1;
                     const float2 q = cs[p][e];
-                    // interleaved units may end in dimensions that are not rotated (q = (1, 0)): they must not meet their
-                    // neighbour's infinity
-                    z0 = q.y == 0.0f ? q.x * x0 : fmaf(-q.y, x1, q.x * x0);
-                    z1 = q.y == 0.0f ? q.x * x1 : fmaf(q.y, x0, q.x * x1);
+                    z0 = fmaf(-q.y, x1, q.x * x0);
+                    z1 = fmaf(q.y, x0, q.x * x1);
+                    // (1, 0) where the unit reaches behind the rotated dimensions: they must not meet their neighbour's
+                    // infinity
+                    if (W == 0 && part_turned && q.y == 0.0f && q.x == 1.0f) {
+                        z0 = x0;
+                        z1 = x1;
+                    }
                 }
             }
 #pragma unroll
             for (int s = 0; s < SIDES; ++s)
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const uint32_t u = __float_as_uint(f[p][s][e]) & 0x7fffffffu;
-                    amax = max(amax, u < 0x7f800000u ? u : 0u);  // infinities saturate, NaN stays: neither sets a scale
-                }
+                for (int e = 0; e < N; ++e) top = fmaxf(top, fabsf(f[p][s][e]));
         }
-        amax = __reduce_max_sync(0xffffffffu, amax);
         uint32_t* const buf = part[h & 1];
-        if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = amax;
-        __syncthreads();  // the other buffer is free: every thread read it before this barrier
-        const int lane = threadIdx.x & 31;
-        amax = __reduce_max_sync(0xffffffffu, lane < warps ? buf[lane] : 0u);
+        auto block_max = [&](float x) -> uint32_t {  // of non-negative numbers, as bits
+            const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(x));
+            if (lane == 0) buf[threadIdx.x >> 5] = w;
+            __syncthreads();
+            return __reduce_max_sync(0xffffffffu, lane < warps ? buf[lane] : 0u);
+        };
+        uint32_t amax = block_max(top);  // the other buffer is free: every thread read it before this barrier
+        if (amax >= 0x7f800000u) {       // infinities saturate: the finite values set the scale
+            top = 0.0f;
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int s = 0; s < SIDES; ++s)
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+                        if (fabsf(f[p][s][e]) < INFINITY) top = fmaxf(top, fabsf(f[p][s][e]));
+            __syncthreads();
+            amax = block_max(top);
+        }
         const int64_t at = (int64_t)page * a.g.kv_heads + h;
         float sc = cache_scale(amax);
         uint8_t* const dst = code + at * C * D;
@@ -238,28 +266,25 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, const T* __rest
         const float inv = 1.0f / sc;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            if (slot[p] < 0) continue;
+            if (!real[p]) continue;
 #pragma unroll
             for (int s = 0; s < SIDES; ++s) {
-                uint8_t* const to = dst + (int64_t)slot[p] * D + dim[p][s];
+                uint8_t* const out = to + p * rows_pass * D + (s ? dim1 - dim0 : 0);
                 const float (&g)[N] = f[p][s];
                 if constexpr (N == 8) {
-                    uint32_t u[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        u[j] = e4m3x2(g[4 * j] * inv, g[4 * j + 1] * inv) |
-                               (e4m3x2(g[4 * j + 2] * inv, g[4 * j + 3] * inv) << 16);
-                    *reinterpret_cast<uint2*>(to) = make_uint2(u[0], u[1]);
+                    *reinterpret_cast<uint2*>(out) =
+                        make_uint2(e4m3x4(g[0] * inv, g[1] * inv, g[2] * inv, g[3] * inv),
+                                   e4m3x4(g[4] * inv, g[5] * inv, g[6] * inv, g[7] * inv));
                 } else if constexpr (N == 4) {
-                    *reinterpret_cast<uint32_t*>(to) =
-                        e4m3x2(g[0] * inv, g[1] * inv) | (e4m3x2(g[2] * inv, g[3] * inv) << 16);
+                    *reinterpret_cast<uint32_t*>(out) = e4m3x4(g[0] * inv, g[1] * inv, g[2] * inv, g[3] * inv);
                 } else if constexpr (N == 2) {
-                    *reinterpret_cast<uint16_t*>(to) = (uint16_t)e4m3x2(g[0] * inv, g[1] * inv);
+                    *reinterpret_cast<uint16_t*>(out) = (uint16_t)e4m3x2(g[0] * inv, g[1] * inv);
                 } else {
-                    *to = (uint8_t)e4m3x2(g[0] * inv, 0.0f);
+                    *out = (uint8_t)e4m3x2(g[0] * inv, 0.0f);
                 }
             }
         }
+        to += C * D;
     }
 }
 
