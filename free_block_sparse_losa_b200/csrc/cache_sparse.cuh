@@ -14,20 +14,26 @@
 //   warp 3       reads order, lists, page table and scales eight tiles at a time (a lane per 32-key quarter, so that the
 //                chain of dependent loads is paid once for eight tiles) into a ring of tile records.
 //   warp 0 / 2   TMA: K / V codes, four 32-key boxes a tile, one per lane.
-//   warps 12..15 split the next item's Q into shared memory one tile ahead, widen V (zeroing keys that do not exist), and
-//                store an item's O from the V slot it was staged in before refilling that slot.
+//   warps 24..27 split an item's Q into shared memory, an item ahead; the reader has its rows fetched into L2.
+//   warps 20..23 widen V (zeroing keys that do not exist), and store an item's O from the V slot it was staged in before
+//                refilling that slot.
 //   warp 1       MMA: S_n = Q K^T into S buffer n & 1, then O += P V of tile n - 2 with P from TMEM.
-//   warps 4..11  softmax in two warpgroups that take the tiles in turn, a thread a whole row: while one group's
-//                exponentials keep the exp unit busy, the other loads its S and finds its maxima. (Both groups on one tile,
-//                half the keys each, run in step: every phase then waits for itself, and each group has to read the other
-//                half of S for the maximum. Measured: 1175 us against 853 us on a 4680-token chunk over 32760 keys.)
-// The row's reference maximum passes from tile to tile through shared memory (M_READY); a group publishes it before its
-// exponentials. It moves only when the maximum exceeds it by more than 2^8; O is then rescaled in place by the group whose
-// tile moved it, behind P V of the tile before. Each group keeps its own share of the denominator; the group with the
-// item's last tile adds the other's, divides and stages O. It does so at once: O's next item waits for it, and the other
-// group works meanwhile.
-// TMEM: S_0 0..127, S_1 128..255, O 256..383, P_0 384..447, P_1 448..511. An S buffer is free once its group has it in
+//   warps 4..19  softmax in two pairs of groups. The pairs take the tiles in turn, a group half of a tile's keys: while one
+//                pair waits for S or finds maxima, the other's exponentials keep the exp unit busy.
+// A row's reference maximum moves only when a tile's maximum exceeds it by more than 2^8. Each group publishes its half's
+// row maxima (M_READY), and every thread follows the reference of its row through the tiles by itself; the pair whose tile
+// moves it rescales O in place, behind P V of the tile before. Each group keeps its own share of the denominator; the pair
+// with the item's last tile adds them up, divides and stages O at once: O's next item waits for it, and the other pair works
+// meanwhile.
+// TMEM: S_0 0..127, S_1 128..255, O 256..383, P_0 384..447, P_1 448..511. An S buffer is free once its pair has it in
 // registers, so Q K^T runs two tiles ahead of P V.
+//
+// Measured on a 4680-token chunk over 32760 keys (12 heads) and on a 480p layer with 16 listed 32-key blocks a row: 1052 and
+// 198 us, 906 and 521 TFLOP/s. Steps that brought it there: one softmax path, keys that do not exist as -inf, and V widened
+// without register swaps (1523 -> 1175 us, 297 -> 252); groups that take tiles in turn instead of halving every tile
+// (-> 1141); MMA issued from uniform registers, four groups and Q split by warps of its own (-> 1052, 259 -> 198). Leaving
+// out half of the MMAs, the exponentials or the widening takes at most a tenth off: no single unit bounds it, but the chain
+// S -> maximum -> weights -> P of two tiles in flight. Three groups of whole rows with P over S are slower (1175, 214 us).
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
