@@ -44,6 +44,7 @@ RopeArgs rope_args(const losa_rope* r) {
 // One side of a rotation: positive extents, strides that keep every 16-byte piece aligned.
 bool view_ok(const losa_token_view* v, int head_dim, int size, bool written) {
     if (!v || v->parts < 1 || v->batch < 1 || v->heads < 1 || v->tokens < 0) return false;
+    if (v->tokens == 0) return true;  // nothing is read or written through it
     const int64_t s[4] = {v->part_stride, v->batch_stride, v->token_stride, v->head_stride};
     const int32_t n[4] = {v->parts, v->batch, v->tokens, v->heads};
     for (int i = 0; i < 4; ++i) {
@@ -200,7 +201,8 @@ losa_status losa_rope_apply(const losa_rope* rope, int32_t dtype, const losa_tok
     if (x_view->parts != y_view->parts || x_view->batch != y_view->batch || x_view->heads != y_view->heads ||
         y_view->tokens < x_view->tokens)
         return LOSA_ERR_INVALID_ARG;
-    if (!aligned16(x) || !aligned16(y) || x == y) return LOSA_ERR_INVALID_ARG;
+    if ((x_view->tokens > 0 && !aligned16(x)) || (y_view->tokens > 0 && (!aligned16(y) || x == y)))
+        return LOSA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(start)) & 3u)
         return LOSA_ERR_INVALID_ARG;
     if ((rope->head_dim * size) % 16 != 0 || x_view->parts > 32 || x_view->batch > 65535 ||

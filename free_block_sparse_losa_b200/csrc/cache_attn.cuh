@@ -545,8 +545,8 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
     unit_pos += (int64_t)(head / a.group * a.tiles + row / a.tile_rows) * n_tiles;
     const int splits =
         n_tiles ? (int)(ca_div(unit_pos + n_tiles - 1, w.range) - ca_div(unit_pos, w.range)) + 1 : 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this grid must not end before that one
     if (splits == 1) return;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const float2* const ml = a.part_ml + id * a.splits;
     float top = -INFINITY;
     for (int s = lane; s < splits; s += 32) top = fmaxf(top, ml[s].x);

@@ -1,6 +1,6 @@
-"""Device-buffer harness around the C ABI: allocates the caller-owned buffers of one attention layer with
-PyTorch (device memory and streams only) and calls the three entry points in order. No computation happens
-here; every step runs in the library's kernels."""
+"""Device-buffer harness around the C ABI: allocates the caller-owned buffers of one attention layer (LayerBuffers) and of
+a layer's paged 8-bit key/value cache (KvCache) with PyTorch (device memory and streams only) and calls the entry points
+in order. No computation happens here; every step runs in the library's kernels."""
 from __future__ import annotations
 
 from dataclasses import dataclass
@@ -8,8 +8,10 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
-from . import (DTYPE_BF16, DTYPE_F32, losa_dense_profile, losa_dense_profile_workspace_bytes, losa_dense_profile_ws,
-               losa_select, losa_select_topk, losa_select_workspace_bytes, losa_sparse_attn, make_shape)
+from . import (DTYPE_BF16, DTYPE_F32, losa_cache_append, losa_cache_attn, losa_cache_attn_workspace_bytes,
+               losa_cache_sparse_attn, losa_dense_profile, losa_dense_profile_workspace_bytes, losa_dense_profile_ws,
+               losa_rope_apply, losa_select, losa_select_topk, losa_select_workspace_bytes, losa_sparse_attn, make_cache,
+               make_shape)
 
 
 def host_tokens_to_device(a: np.ndarray, dtype: str, device="cuda") -> torch.Tensor:
@@ -82,7 +84,74 @@ class LayerBuffers:
         losa_sparse_attn(self.shape, q, k, v, scale, self.indptr, self.kv_idx, self.order if order else None,
                          self.o if out is None else out, lse, stream=stream)
 
+    def pack_qkv(self, qkv, rope, out=None, positions=None, start=None, stream=None):
+        """A fused projection's output (batch, N, 3, heads / batch, d), any strides but a contiguous last dimension, as the
+        calls' q, k, v: query and key rotated, head-major, padding rows zero. Returns views of one (3, H, Np, d) buffer."""
+        batch, n, _, heads, d = qkv.shape
+        if out is None:
+            out = torch.empty((3, self.heads, self.n_padded, self.head_dim), dtype=qkv.dtype, device=qkv.device)
+        y = out.view(3, batch, heads, self.n_padded, d).permute(0, 1, 3, 2, 4)
+        losa_rope_apply(rope, qkv.permute(2, 0, 1, 3, 4), y, rotate=0b011, positions=positions, start=start, stream=stream)
+        return out[0], out[1], out[2]
+
+    def unpack_o(self, rope, out, o=None, stream=None):
+        """The head-major output's real rows into out (batch, N, heads / batch, d), for the output projection."""
+        batch, n, heads, d = out.shape
+        o = (self.o if o is None else o).view(1, batch, heads, self.n_padded, d).permute(0, 1, 3, 2, 4)[:, :, :n]
+        losa_rope_apply(rope, o, out[None], rotate=0, stream=stream)
+        return out
+
     def csr_host(self):
         indptr = self.indptr.cpu().numpy()
         nnz = int(indptr[-1])
         return indptr, self.kv_idx[:nnz].cpu().numpy(), self.order.cpu().numpy()
+
+
+class KvCache:
+    """A layer's paged 8-bit cache for `seqs` sequences of up to `capacity` tokens: its pool, page table (each sequence's
+    pages in order) and lengths, which live on the device. max_len bounds the lengths on the host."""
+
+    def __init__(self, seqs, kv_heads, head_dim, capacity, page_tokens=128, rope=None, device="cuda"):
+        self.seqs, self.page_tokens, self.rope = seqs, page_tokens, rope
+        width = -(-capacity // page_tokens)
+        self.cache = make_cache(kv_heads, head_dim, page_tokens, seqs * width, seqs, width)
+        pool = (seqs * width, kv_heads, page_tokens, head_dim)
+        self.k8 = torch.zeros(pool, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+        self.v8 = torch.zeros(pool, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+        self.k_scale = torch.ones(pool[:2], dtype=torch.float32, device=device)
+        self.v_scale = torch.ones(pool[:2], dtype=torch.float32, device=device)
+        self.page_table = torch.arange(seqs * width, dtype=torch.int32, device=device).view(seqs, width)
+        self._lens = torch.zeros((2, seqs), dtype=torch.int32, device=device)
+        self._now = 0
+        self.max_len = 0
+        self._workspace = torch.empty(16, dtype=torch.uint8, device=device)
+
+    @property
+    def lens(self):
+        return self._lens[self._now]
+
+    @property
+    def buffers(self):
+        return self.k8, self.v8, self.k_scale, self.v_scale, self.page_table
+
+    def append(self, k, v, new_tokens, indptr=None, positions=None, stream=None):
+        """k, v: (tokens, kv_heads, d) of all sequences; new_tokens of each, or at most that many with indptr."""
+        nxt = 1 - self._now
+        losa_cache_append(self.cache, k, v, *self.buffers, self.lens, new_tokens, indptr=indptr, new_lens=self._lens[nxt],
+                          rope=self.rope, positions=positions, stream=stream)
+        self._now = nxt
+        self.max_len = min(self.max_len + int(new_tokens), self.cache.table_stride * self.page_tokens)
+
+    def attend(self, q, scale, o, lse=None, causal=True, stream=None):
+        """The last tokens q (seqs, tokens, heads, d), appended before, over the whole cache."""
+        need = losa_cache_attn_workspace_bytes(self.cache, q.shape[2], q.shape[1], self.max_len)
+        if need > self._workspace.numel():
+            self._workspace = torch.empty(need, dtype=torch.uint8, device=self.k8.device)
+        losa_cache_attn(self.cache, q, *self.buffers, self.lens, scale, o, lse=lse, causal=causal, max_len=self.max_len,
+                        workspace=self._workspace, stream=stream)
+
+    def sparse(self, layer, q, scale, out, lse=None, lists=True, order=True, stream=None):
+        """Query blocks of a layer (LayerBuffers with block_k = page_tokens) over its frozen lists, or over every block."""
+        losa_cache_sparse_attn(layer.shape, self.cache, q, *self.buffers, self.lens, scale, out,
+                               indptr=layer.indptr if lists else None, kv_block_idx=layer.kv_idx if lists else None,
+                               order=layer.order if lists and order else None, lse=lse, stream=stream)

@@ -271,7 +271,7 @@ losa_status losa_cache_append(const losa_cache* cache, const losa_rope* rope, in
  *   q, o      : bf16, element (b, i, h, e) at b seq_stride + i token_stride + h head_stride + e; strides are multiples of 8
  *               elements. o must not overlap q.
  *   scale     : logit scale, > 0.
- *   max_len   : an upper bound of lens, by which the work is split; results do not depend on it being one. <= 0: the
+ *   max_len   : an upper bound of lens, by which the work is split (a wrong one costs time, not accuracy). <= 0: the
  *               table's capacity.
  *   lse       : [seqs][tokens][heads] fp32 or NULL.
  *   workspace : scratch of losa_cache_attn_workspace_bytes(cache, heads, tokens, max_len) bytes, 16-byte aligned (may be

@@ -563,3 +563,215 @@ def test_cache_sparse_attn_reports_bad_input():
             key = torch.cat([torch.arange(j * page, j * page + page, device="cuda") for j in left])
             want, wl, size = attend(q[0, :128].double(), k[key], v[key], torch.full((128,), len(key), device="cuda"), 0.02)
             attn_close(o[0, :128], lse[0, :128], want, wl, size)
+
+
+# ------------------------------------------------------------------------------------------- together, streams, graphs
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [128, 32])
+def test_a_stream_of_chunks_end_to_end(page):
+    """A clip generated in two chunks and then token by token, through the harness: projection -> rotated layer ->
+    pattern from the exact masses -> 8-bit cache -> sparse attention over the frozen lists -> token-major output; then
+    three drafted tokens decoded over everything. Every step against 64 bits on what the step before stored."""
+    require_gpu()
+    from free_block_sparse_losa_b200.harness import KvCache, LayerBuffers
+    g = gen(21)
+    H, d, n, gy, gx = 3, 128, 2 * 13 * 21, 13, 21
+    scale = 1 / math.sqrt(d)
+    rope = L.make_rope(d, (44, 42, 42), (gy, gx))
+    cache = KvCache(1, H, d, 2 * n + 64, page_tokens=page, rope=rope)
+    qkv = torch.randn(1, 2 * n, 3, H, d, generator=g, device="cuda").bfloat16()
+    qkv[:, :, :2] *= 1.5
+    np_ = -(-n // 128) * 128
+    layer = LayerBuffers(H, n, np_, d, 128, "bf16", block_k=page if page == 32 else 0)
+    for chunk in range(2):
+        part = qkv[:, chunk * n:(chunk + 1) * n]
+        start = torch.tensor([chunk * n], dtype=torch.int32, device="cuda")
+        q, k, v = layer.pack_qkv(part, rope, start=start)
+        pos = grid_positions(chunk * n + torch.arange(n), gy, gx)
+        want = turn(part[0, :, 0].double(), pos[:, None], (44, 42, 42), False).transpose(0, 1)
+        assert bool(((q[:, :n].double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-5).all())
+        assert not k[:, n:].any() and torch.equal(v[:, :n], part[0, :, 2].transpose(0, 1))
+        if chunk == 0:
+            layer.profile(q, k, v, scale)
+            layer.select(0.95)
+        cache.append(part[0, :, 1], part[0, :, 2], n)
+        assert cache.lens.tolist() == [(chunk + 1) * n]
+        o, lse = torch.empty_like(q), torch.empty(H, np_, device="cuda")
+        cache.sparse(layer, q, scale, o, lse=lse)  # the second chunk reuses the frozen lists
+        assert L.losa_get_device_error() == 0
+        check_blocks(q, o, lse, (cache.k8, cache.v8, cache.k_scale, cache.v_scale), cache.page_table, cache.lens.tolist(),
+                     page, H, H, n, scale, layer.indptr, layer.kv_idx)
+        back = layer.unpack_o(rope, torch.empty(1, n, H, d, dtype=torch.bfloat16, device="cuda"), o=o)
+        assert torch.equal(back[0].transpose(0, 1), o[:, :n])
+        if chunk == 0:  # the 8-bit step stays near the 16-bit one: e4m3 values are off by at most 2^-4, on average far less
+            ref = torch.empty_like(q)
+            layer.sparse(q, k, v, scale, out=ref)
+            rel = (o[:, :n].float() - ref[:, :n].float()).norm() / ref[:, :n].float().norm()
+            assert float(rel) <= 2.0 ** -4
+    for step in range(2):
+        new = torch.randn(3, 3, H, d, generator=g, device="cuda").bfloat16()
+        base = 2 * n + 3 * step
+        q = torch.empty(1, 3, H, d, dtype=torch.bfloat16, device="cuda")
+        L.losa_rope_apply(rope, new[:, 0][None, None], q[None], start=cache.lens)
+        cache.append(new[:, 1], new[:, 2], 3)
+        o, lse = torch.empty_like(q), torch.empty(1, 3, H, device="cuda")
+        cache.attend(q, scale, o, lse=lse)
+        assert cache.lens.tolist() == [base + 3] and L.losa_get_device_error() == 0
+        for h in range(H):
+            k = dense(cache.k8, cache.k_scale, cache.page_table, 0, h, base + 3)
+            v = dense(cache.v8, cache.v_scale, cache.page_table, 0, h, base + 3)
+            end = torch.tensor([base + 1, base + 2, base + 3], device="cuda")
+            want, wl, size = attend(q[0, :, h].double(), k, v, end, scale)
+            attn_close(o[0, :, h], lse[0, :, h], want, wl, size)
+        # what the cache holds is the rotated keys, to within the rounding of their block's scale
+        pos = grid_positions(base + torch.arange(3), gy, gx)
+        keys = turn(new[:, 1].double(), pos[:, None], (44, 42, 42), False)
+        got = torch.stack([dense(cache.k8, cache.k_scale, cache.page_table, 0, h, base + 3)[-3:] for h in range(H)], 1)
+        top = keys.abs().amax() * 2  # a block's scale is below twice what its loudest key needs
+        assert bool(((got - keys).abs() <= 2.0 ** -4 * keys.abs() + 2.0 ** -9 * 4 * top / 448 + 2.0 ** -4 * top / 64).all())
+
+
+@pytest.mark.gpu
+def test_calls_on_other_streams_with_their_own_workspaces():
+    """The same decode from four streams at once, each with its own inputs, outputs and workspace, gives what one stream
+    gives, bit for bit; the blocked form and the append run beside them."""
+    require_gpu()
+    g = gen(31)
+    lens, hk, page, d = [5000, 9000], 2, 64, 128
+    width = -(-max(lens) // page)
+    pool = poisoned_cache(g, lens, hk, page, d, width)
+    k8, v8, ks, vs, table = pool
+    cache = L.make_cache(hk, d, page, k8.shape[0], 2, width)
+    lens_t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    need = L.losa_cache_attn_workspace_bytes(cache, 4, 2, max(lens))
+    assert need > 0
+    runs = []
+    for _ in range(4):
+        q = torch.randn(2, 2, 4, d, generator=g, device="cuda").bfloat16()
+        runs.append([q, torch.empty_like(q), torch.empty(need, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()])
+    qb = torch.randn(8, 256, 128, generator=g, device="cuda").bfloat16()
+    shape = L.make_shape(8, 256, 256, 128, 128, page, "bf16")
+    ob = torch.empty_like(qb)
+
+    def decode(q, o, ws, stream=None):
+        L.losa_cache_attn(cache, q, k8, v8, ks, vs, table, lens_t, 0.02, o, max_len=max(lens), workspace=ws, stream=stream)
+
+    want = []
+    for q, o, ws, _ in runs:
+        decode(q, o, ws)
+        want.append(o.clone())
+    L.losa_cache_sparse_attn(shape, cache, qb, k8, v8, ks, vs, table, lens_t, 0.02, ob)
+    want_b = ob.clone()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for q, o, ws, st in runs:
+            o.zero_()
+        ob.zero_()
+        torch.cuda.synchronize()
+        for q, o, ws, st in runs:
+            decode(q, o, ws, stream=st)
+        with torch.cuda.stream(runs[0][3]):
+            L.losa_cache_sparse_attn(shape, cache, qb, k8, v8, ks, vs, table, lens_t, 0.02, ob)
+        torch.cuda.synchronize()
+        assert all(torch.equal(r[1], w) for r, w in zip(runs, want)) and torch.equal(ob, want_b)
+    assert L.losa_get_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_captured_steps_replayed_on_new_inputs():
+    """A captured step (rotation, append, decode over the grown cache, blocked attention) replayed with new tokens and new
+    lengths in place gives what eager calls give."""
+    require_gpu()
+    g = gen(41)
+    hk, page, d, H = 2, 32, 128, 4
+    width = 40
+    pages = 2 * width
+    cache = L.make_cache(hk, d, page, pages, 2, width)
+    rope = L.make_rope(d, (16, 56, 56), (3, 7), halves=True)
+    table = torch.randperm(pages, generator=g, device="cuda").view(2, width).int()
+    shape = L.make_shape(2 * H, 100, 128, 128, 128, page, "bf16")
+
+    def state(seed):
+        z = gen(seed)
+        return dict(pool=make_pool(gen(99), pages, hk, page, d), lens=torch.tensor([40 + seed, 1100], dtype=torch.int32, device="cuda"),
+                    new=torch.zeros(2, dtype=torch.int32, device="cuda"),
+                    x=torch.randn(2, 2, H + 2 * hk, d, generator=z, device="cuda").bfloat16(),
+                    q=torch.zeros(2, 2, H, d, device="cuda").bfloat16(), o=torch.zeros(2, 2, H, d, device="cuda").bfloat16(),
+                    qb=torch.randn(2 * H, 128, d, generator=z, device="cuda").bfloat16(),
+                    ob=torch.zeros(2 * H, 128, d, device="cuda").bfloat16(),
+                    ws=torch.empty(max(16, L.losa_cache_attn_workspace_bytes(cache, H, 2)), dtype=torch.uint8, device="cuda"))
+
+    def step(s):
+        L.losa_rope_apply(rope, s["x"][None, :, :, :H], s["q"][None], start=s["lens"])
+        kv = s["x"].view(4, H + 2 * hk, d)
+        L.losa_cache_append(cache, kv[:, H:H + hk], kv[:, H + hk:], *s["pool"], table, s["lens"], 2, new_lens=s["new"], rope=rope)
+        L.losa_cache_attn(cache, s["q"], *s["pool"], table, s["new"], 0.05, s["o"], workspace=s["ws"])
+        L.losa_cache_sparse_attn(shape, cache, s["qb"], *s["pool"], table, s["new"], 0.05, s["ob"])
+
+    a = state(1)
+    step(a)  # loads the kernels
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    a = state(1)
+    with torch.cuda.graph(graph, stream=side):
+        step(a)
+    for seed in (2, 3):
+        b = state(seed)
+        step(b)
+        fresh = state(seed)
+        for key in ("lens", "x", "qb"):
+            a[key].copy_(fresh[key])
+        for dst, src in zip(a["pool"], fresh["pool"]):
+            dst.view(torch.uint8).copy_(src.view(torch.uint8)) if dst.dtype == torch.float8_e4m3fn else dst.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        for key in ("new", "q", "o", "ob"):
+            assert torch.equal(a[key], b[key]), key
+        assert all(torch.equal(u.view(torch.uint8), w.view(torch.uint8)) for u, w in zip(a["pool"], b["pool"]))
+    assert L.losa_get_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_offsets_beyond_32_bits():
+    """A pool of more than 2^31 codes and a rotation of more than 2^31 elements: the far ends are read and written."""
+    require_gpu()
+    g = gen(51)
+    hk, page, d = 8, 128, 128
+    pages = (2 ** 31) // (hk * page * d) + 64
+    assert pages * hk * page * d > 2 ** 31
+    k8 = torch.zeros(pages, hk, page, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    v8 = torch.zeros(pages, hk, page, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    ks, vs = torch.ones(pages, hk, device="cuda"), torch.ones(pages, hk, device="cuda")
+    table = torch.tensor([[pages - 1, 0, pages - 2]], dtype=torch.int32, device="cuda")
+    cache = L.make_cache(hk, d, page, pages, 1, 3)
+    n = 300
+    kv = torch.randn(n, 2, hk, d, generator=g, device="cuda").bfloat16()
+    lens, new = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    L.losa_cache_append(cache, kv[:, 0], kv[:, 1], k8, v8, ks, vs, table, lens, n, new_lens=new)
+    q = torch.randn(1, 2, hk, d, generator=g, device="cuda").bfloat16()
+    o = torch.empty_like(q)
+    ws = torch.empty(max(16, L.losa_cache_attn_workspace_bytes(cache, hk, 2)), dtype=torch.uint8, device="cuda")
+    L.losa_cache_attn(cache, q, k8, v8, ks, vs, table, new, 0.05, o, workspace=ws)
+    qb = torch.randn(hk, 128, d, generator=g, device="cuda").bfloat16()
+    ob, lb = torch.empty_like(qb), torch.empty(hk, 128, device="cuda")
+    L.losa_cache_sparse_attn(L.make_shape(hk, 128, 128, d, 128, page, "bf16"), cache, qb, k8, v8, ks, vs, table, new, 0.05, ob,
+                             lse=lb)
+    assert L.losa_get_device_error() == 0
+    for h in (0, hk - 1):
+        k, v = dense(k8, ks, table, 0, h, n), dense(v8, vs, table, 0, h, n)
+        assert float((k - kv[:, 0, h].double()).abs().max()) <= 2.0 ** -4 * float(kv.abs().max())
+        want, _, size = attend(q[0, :, h].double(), k, v, torch.tensor([n - 1, n], device="cuda"), 0.05)
+        assert bool(((o[0, :, h].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * size).all())
+        want, wl, size = attend(qb[h].double(), k, v, torch.full((128,), n, device="cuda"), 0.05)
+        attn_close(ob[h], lb[h], want, wl, size)
+    del k8, v8
+    heads, n = 128, 131100
+    x = torch.zeros(1, 1, n, heads, d, dtype=torch.bfloat16, device="cuda")
+    x[0, 0, -3:] = torch.randn(3, heads, d, generator=g, device="cuda").bfloat16()
+    y = torch.empty(1, 1, heads, n, d, dtype=torch.bfloat16, device="cuda")
+    assert x.numel() > 2 ** 31
+    L.losa_rope_apply(L.make_rope(d, (44, 42, 42), (45, 80)), x, y.transpose(2, 3))
+    want = turn(x[0, 0, -3:].double(), grid_positions(n - 3 + torch.arange(3), 45, 80)[:, None], (44, 42, 42), False)
+    assert bool(((y[0, 0, :, -3:].transpose(0, 1).double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-5).all())
+    assert not y[0, 0, :, :-3].any()
