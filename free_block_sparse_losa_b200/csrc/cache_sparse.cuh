@@ -58,10 +58,10 @@ struct CsTile {
     float ks[4], lv[4], iv[4];  // scale of K, log2 and reciprocal of V's
     uint32_t kv4;       // keys that exist in each quarter, 8 bits each
     int32_t qrow;       // first row of the query block in [H * Np]
-    int32_t flags;      // kCsFirst, kCsLast, kCsPre; negative: past the end of this CTA's work
-    int32_t pad;
+    int32_t flags;      // of the tile in its item; negative: past the end of this CTA's work
+    int32_t item;       // number of the item in this CTA's work
 };
-constexpr int kCsFirst = 1, kCsLast = 2, kCsPre = 4;  // first, last, last but one tile of its item
+constexpr int kCsFirst = 1, kCsSecond = 2, kCsPre = 4, kCsLast = 8;  // first, second, last but one, last tile of an item
 static_assert(sizeof(CsTile) == 80, "tile record");
 
 constexpr uint32_t kCsFac = kCsRec + kCsBatch * kCsBatches * sizeof(CsTile);  // [4][128] reciprocal row factors
@@ -132,6 +132,17 @@ __host__ __device__ constexpr uint32_t idesc_fmt0_f32(int M, int N, bool b_mn_ma
     return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+__device__ __forceinline__ bool cs_wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
+    return wait_bounded_warp(bar, parity, limit_ns);
+}
+// Two barriers, both tested before either answer is looked at.
+__device__ __forceinline__ bool cs_wait2(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
+                                         unsigned long long limit_ns) {
+    const bool ok0 = mbar_try_wait(bar0, parity0), ok1 = mbar_try_wait(bar1, parity1);
+    if (__all_sync(0xffffffffu, ok0 && ok1)) return true;
+    return cs_wait(bar0, parity0, limit_ns) && cs_wait(bar1, parity1, limit_ns);
+}
+
 constexpr float kCsBias = 7.0f;   // weights are kept at 2^7 of their size: at most 2^15 when the reference lags by 2^8
 
 __global__ void __launch_bounds__(kCsThreads, 1)
@@ -186,7 +197,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
     // back after its last tile.
     auto record = [&](uint32_t n) -> const CsTile* {
         const uint32_t k = n / kCsBatch, sl = k % kCsBatches;
-        if (n % kCsBatch == 0 && !wait_bounded_warp(BAR(C_REC_FULL0 + sl), (k / kCsBatches) & 1u, lim)) return nullptr;
+        if (n % kCsBatch == 0 && !cs_wait(BAR(C_REC_FULL0 + sl), (k / kCsBatches) & 1u, lim)) return nullptr;
         return &recs[sl * kCsBatch + n % kCsBatch];
     };
     auto release = [&](uint32_t n) {
@@ -205,11 +216,13 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             int r = 0;                       // next round
             int w_id = -1, w_begin = 0, w_count = 0;  // this lane's item of the current window of 32 rounds
             int id = 0, begin = 0, count = 0, tiles = 0, t = 0;  // the current item
-            bool ended = false;
-            for (uint32_t k = 0; !ended; ++k) {
+            int items = -1;                  // its number
+            bool ended = false, seen = false;  // seen: both parities of tiles have an end record
+            for (uint32_t k = 0; !seen; ++k) {
                 const uint32_t sl = k % kCsBatches;
-                if (!wait_bounded_warp(BAR(C_REC_EMPTY0 + sl), ((k / kCsBatches) & 1u) ^ 1u, lim)) break;
-                int m_id = 0, m_begin = 0, m_count = 0, m_t = 0, m_flags = -1;  // tile `lane` of the batch
+                if (!cs_wait(BAR(C_REC_EMPTY0 + sl), ((k / kCsBatches) & 1u) ^ 1u, lim)) break;
+                int m_id = 0, m_begin = 0, m_count = 0, m_t = 0, m_flags = -1, m_item = 0;  // tile `lane` of the batch
+                seen = ended;
                 for (int i = 0; i < kCsBatch && !ended; ++i) {
                     while (t == tiles && !ended) {  // next item
                         if ((r & 31) == 0) {
@@ -243,21 +256,27 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                         ++r;
                         t = 0;
                         tiles = id == -2 ? 0 : max(1, (count + a.sub - 1) / a.sub);  // an empty list still writes its rows
-                        if (id == -1) ended = true;
+                        if (tiles > 0) ++items;
+                        if (id == -1) {
+                            ended = true;
+                            seen = i < kCsBatch - 1;
+                        }
                     }
                     if ((int)lane == i && !ended) {
                         m_id = id;
                         m_begin = begin;
                         m_count = count;
                         m_t = t;
-                        m_flags = (t == 0 ? kCsFirst : 0) | (t == tiles - 1 ? kCsLast : 0) | (t == tiles - 2 ? kCsPre : 0);
+                        m_flags = (t == 0 ? kCsFirst : 0) | (t == 1 ? kCsSecond : 0) | (t == tiles - 2 ? kCsPre : 0) |
+                                  (t == tiles - 1 ? kCsLast : 0);
+                        m_item = items;
                     }
                     ++t;
                 }
                 const int src = (int)lane >> 2, g = (int)lane & 3;
                 const int q_id = __shfl_sync(0xffffffffu, m_id, src), q_begin = __shfl_sync(0xffffffffu, m_begin, src);
                 const int q_count = __shfl_sync(0xffffffffu, m_count, src), q_t = __shfl_sync(0xffffffffu, m_t, src);
-                const int q_flags = __shfl_sync(0xffffffffu, m_flags, src);
+                const int q_flags = __shfl_sync(0xffffffffu, m_flags, src), q_item = __shfl_sync(0xffffffffu, m_item, src);
                 const int h = q_id / a.nq, seq = h / a.heads, kvh = (h - seq * a.heads) / a.group;
                 int valid = 0, row = 0;
                 float ks = 1.0f, vs = 1.0f;
@@ -297,6 +316,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 if (g == 0) {
                     rec->qrow = h * a.Np + (q_id - h * a.nq) * kTcRows;
                     rec->flags = q_flags;
+                    rec->item = q_item;
                     if (q_flags >= 0 && (q_flags & kCsFirst))  // warps 24..27 read it some tiles from now
                         l2_prefetch(a.q + (size_t)rec->qrow * kTcDim, kTileBytes);
                 }
@@ -316,7 +336,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 const CsTile* const rec = record(n);
                 if (!rec || rec->flags < 0) break;
                 const uint32_t s = n % stages;
-                if (!wait_bounded_warp(BAR(empty + s), ((n / stages) & 1u) ^ 1u, lim)) break;
+                if (!cs_wait(BAR(empty + s), ((n / stages) & 1u) ^ 1u, lim)) break;
                 if (lane == 0) mbar_arrive_expect_tx(BAR(full + s), kCsTile8);
                 __syncwarp();
                 if (lane < 4)
@@ -341,10 +361,9 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             auto issue_pv = [&]() -> bool {  // tile pv
                 const uint32_t b = pv & 1u, par = (pv >> 1) & 1u;
                 const bool first = (firsts >> (pv & 31u)) & 1u;
-                if (!wait_bounded_warp(BAR(C_P_FULL0 + b), par, lim)) return false;
-                if (!wait_bounded_warp(BAR(C_VF_FULL0 + b), par, lim)) return false;
+                if (!cs_wait2(BAR(C_P_FULL0 + b), par, BAR(C_VF_FULL0 + b), par, lim)) return false;
                 if (first) {
-                    if (pv_items > 0 && !wait_bounded_warp(BAR(C_O_FREE), (pv_items - 1) & 1u, lim)) return false;
+                    if (pv_items > 0 && !cs_wait(BAR(C_O_FREE), (pv_items - 1) & 1u, lim)) return false;
                     ++pv_items;
                 }
                 tc_fence_after();
@@ -357,21 +376,24 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 return true;
             };
             bool ok = true;
-            for (;; ++n) {
-                const CsTile* const rec = record(n);
-                if (!(ok = rec != nullptr)) break;
-                const int flags = __shfl_sync(0xffffffffu, rec->flags, 0);
-                if (flags < 0) break;
-                release(n);
-                firsts = (firsts & ~(1u << (n & 31u))) | ((uint32_t)(flags & kCsFirst) << (n & 31u));
-                if (flags & kCsFirst) {
+            int flags = -1;
+            auto look = [&](uint32_t x) -> bool {  // flags of tile x
+                const CsTile* const rec = record(x);
+                if (!rec) return false;
+                flags = __shfl_sync(0xffffffffu, rec->flags, 0);
+                release(x);
+                return true;
+            };
+            for (ok = look(0); ok && flags >= 0; ++n) {
+                const uint32_t first = flags & kCsFirst, last = flags & kCsLast;
+                firsts = (firsts & ~(1u << (n & 31u))) | (first << (n & 31u));
+                if (first) {
                     ++items;
-                    if (!(ok = wait_bounded_warp(BAR(C_Q_FULL0 + ((items - 1) & 1u)), ((items - 1) >> 1) & 1u, lim)))
-                        break;
+                    if (!(ok = cs_wait(BAR(C_Q_FULL0 + ((items - 1) & 1u)), ((items - 1) >> 1) & 1u, lim))) break;
                 }
                 const uint32_t qs = (items - 1) & 1u, ks = n % kCsKStages, b = n & 1u;
-                if (!(ok = wait_bounded_warp(BAR(C_K_FULL0 + ks), (n / kCsKStages) & 1u, lim))) break;
-                if (!(ok = wait_bounded_warp(BAR(C_S_FREE0 + b), ((n >> 1) & 1u) ^ 1u, lim))) break;
+                if (!(ok = cs_wait2(BAR(C_K_FULL0 + ks), (n / kCsKStages) & 1u, BAR(C_S_FREE0 + b), ((n >> 1) & 1u) ^ 1u, lim)))
+                    break;
                 tc_fence_after();
                 const uint64_t dQ = dQ0 + qs * (2 * kCsTile8 >> 4), dK = dK0 + ks * (kCsTile8 >> 4);
 #pragma unroll
@@ -380,12 +402,13 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                                  kIdQK, kk ? 1u : 0u);
                 el_commit(BAR(C_S_FULL0 + b));
                 el_commit(BAR(C_K_EMPTY0 + ks));
-                if (flags & kCsLast) el_commit(BAR(C_Q_EMPTY0 + qs));
+                if (last) el_commit(BAR(C_Q_EMPTY0 + qs));
+                if (!(ok = look(n + 1))) break;
                 if (n >= 2 && !(ok = issue_pv())) break;
             }
             while (ok && pv < n) ok = issue_pv();
             el_commit(BAR(C_MMA_DONE));
-            wait_bounded_warp(BAR(C_MMA_DONE), 0, kDrainLimitNs);
+            cs_wait(BAR(C_MMA_DONE), 0, kDrainLimitNs);
         }
     } else if (warp >= 24) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
@@ -402,7 +425,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             release(n);
             if (!first) continue;
             const uint32_t qs = items & 1u;
-            if (!wait_bounded_warp(BAR(C_Q_EMPTY0 + qs), ((items >> 1) & 1u) ^ 1u, lim)) break;
+            if (!cs_wait(BAR(C_Q_EMPTY0 + qs), ((items >> 1) & 1u) ^ 1u, lim)) break;
             const uint32_t dst = base + kCsQ + qs * 2 * kCsTile8;
 #pragma unroll 1
             for (uint32_t i = 0; i < 4; ++i) {
@@ -462,7 +485,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
         uint32_t staged[2] = {0, 0}, flushed[2] = {0, 0};
         // The O staged in slot sl leaves for global memory; returns once the slot has been read.
         auto flush = [&](uint32_t sl) -> bool {
-            if (!wait_bounded_warp(BAR(C_STAGED0 + sl), staged[sl] & 1u, lim)) return false;
+            if (!cs_wait(BAR(C_STAGED0 + sl), staged[sl] & 1u, lim)) return false;
             ++staged[sl];
             if (warp == 20 && lane == 0) {
                 tma_store_2d(&tmO, base + kCsVf + sl * kTileBytes, 0, fin_row[sl]);
@@ -472,7 +495,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 mbar_arrive(BAR(C_FLUSHED0 + sl));
             }
             __syncwarp();
-            if (!wait_bounded_warp(BAR(C_FLUSHED0 + sl), flushed[sl] & 1u, lim)) return false;
+            if (!cs_wait(BAR(C_FLUSHED0 + sl), flushed[sl] & 1u, lim)) return false;
             ++flushed[sl];
             fin[sl] = false;
             return true;
@@ -493,10 +516,10 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             const uint32_t b = n & 1u, par = (n >> 1) & 1u;
             if (n >= 2) {
                 if (fin[b]) ok = flush(b);
-                else ok = wait_bounded_warp(BAR(C_PV_DONE0 + b), ((n - 2) >> 1) & 1u, lim);
+                else ok = cs_wait(BAR(C_PV_DONE0 + b), ((n - 2) >> 1) & 1u, lim);
                 if (!ok) break;
             }
-            if (!(ok = wait_bounded_warp(BAR(C_V8_FULL0 + b), par, lim))) break;
+            if (!(ok = cs_wait(BAR(C_V8_FULL0 + b), par, lim))) break;
             const uint32_t src = base + kCsV8 + b * kCsTile8 + wt * 4096u;
             const uint32_t dst = base + kCsVf + b * kTileBytes + (c16 >> 2) * kBoxBytes + wt * 4096u;
 #pragma unroll
@@ -535,21 +558,15 @@ __global__ void __launch_bounds__(kCsThreads, 1)
         // A row's reference after a tile whose maximum is top: it moves when the row sees its first key, or when the
         // maximum exceeds it by more than 2^8. Every thread of a row follows it through all tiles by itself.
         auto moved = [](float m, float top) { return m == -INFINITY || top - m > 8.0f ? top : m; };
-        uint32_t items = 0;
         float l = 0.0f, m = -INFINITY;  // this thread's share of the item's denominator, and its reference
-        bool fresh = true;              // no tile of this item has come to this pair yet
-        for (uint32_t n = 0;; ++n) {
-            const CsTile* const rec = record(n);
-            if (!rec || rec->flags < 0) break;
+        for (uint32_t n = pair;; n += 2) {
+            const uint32_t k = n / kCsBatch, sl = k % kCsBatches;
+            if (n % kCsBatch < 2 && !cs_wait(BAR(C_REC_FULL0 + sl), (k / kCsBatches) & 1u, lim)) break;
+            const CsTile* const rec = &recs[sl * kCsBatch + n % kCsBatch];
             const int flags = rec->flags;
-            if (flags & kCsFirst) {
-                ++items;
-                fresh = true;
-            }
-            if ((n & 1u) != pair) {
-                release(n);
-                continue;
-            }
+            if (flags < 0) break;
+            const uint32_t item = (uint32_t)rec->item;
+            const bool fresh = flags & (kCsFirst | kCsSecond);  // no tile of this item has come to this pair yet
             const uint32_t par = (n >> 1) & 1u;
             const int32_t qrow = rec->qrow;
             const uint32_t kv2 = (rec->kv4 >> (16 * half)) & 0xffffu;
@@ -560,14 +577,17 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 lv[x] = rec->lv[2 * half + x];
                 iv[x] = rec->iv[2 * half + x];
             }
-            release(n);
-            if (!wait_bounded_warp(BAR(C_S_FULL0 + pair), par, lim)) break;
+            if (n % kCsBatch >= kCsBatch - 2) {  // this pair's last tile of the batch
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(C_REC_EMPTY0 + sl));
+            }
+            if (!cs_wait(BAR(C_S_FULL0 + pair), par, lim)) break;
             tc_fence_after();
             float s[64];
             tmem_ld32(tSb, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
             tmem_ld32(tSb + 32u, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
             // the row's factor was written before Q K^T could start
-            const float c = fmaxf(a.scale_log2 * fac[((items - 1) & 3u) * 128u + (uint32_t)row], 1e-37f);
+            const float c = fmaxf(a.scale_log2 * fac[(item & 3u) * 128u + (uint32_t)row], 1e-37f);
             tmem_wait_ld();
             tc_fence_before();
             mbar_arrive(BAR(C_S_FREE0 + pair));
@@ -593,7 +613,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             }
             // The tile before first, then this one: a pair that published a tile before it had seen the other's could run
             // two phases ahead of a reader.
-            if (n > 0 && !wait_bounded_warp(BAR(C_M_READY0 + (pair ^ 1u)), ((n - 1) >> 1) & 1u, lim)) break;
+            if (n > 0 && !cs_wait(BAR(C_M_READY0 + (pair ^ 1u)), ((n - 1) >> 1) & 1u, lim)) break;
             float* const at = tops + (n & 3u) * 256u + (uint32_t)row;
             at[half * 128u] = top;
             mbar_arrive(BAR(C_M_READY0 + pair));
@@ -602,16 +622,15 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 const float* const was = tops + ((n - 1) & 3u) * 256u + (uint32_t)row;
                 before = moved(fresh ? -INFINITY : m, fmaxf(was[0], was[128]));
             }
-            if (!wait_bounded_warp(BAR(C_M_READY0 + pair), par, lim)) break;
+            if (!cs_wait(BAR(C_M_READY0 + pair), par, lim)) break;
             const float now = moved(before, fmaxf(top, at[(half ^ 1u) * 128u]));
             if (fresh) l = 0.0f;
             else if (now != m) l *= m == -INFINITY ? 0.0f : ex2_approx(m - now);
             const bool rescale = !(flags & kCsFirst) && now != before && before != -INFINITY;
-            fresh = false;
             m = now;
             const float ref = m == -INFINITY ? 0.0f : kCsBias - m;
             // P's buffer was last read by P V of this pair's tile before
-            if (n >= 2 && !wait_bounded_warp(BAR(C_PV_DONE0 + pair), ((n - 2) >> 1) & 1u, lim)) break;
+            if (n >= 2 && !cs_wait(BAR(C_PV_DONE0 + pair), ((n - 2) >> 1) & 1u, lim)) break;
             tc_fence_after();
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -636,7 +655,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             }
             // O is rescaled once P V of tile n - 1 has added to it
             if (__any_sync(0xffffffffu, rescale)) {
-                if (!wait_bounded_warp(BAR(C_PV_DONE0 + (pair ^ 1u)), ((n - 1) >> 1) & 1u, lim)) break;
+                if (!cs_wait(BAR(C_PV_DONE0 + (pair ^ 1u)), ((n - 1) >> 1) & 1u, lim)) break;
                 tc_fence_after();
                 const float alpha = rescale ? ex2_approx(before - now) : 1.0f;
 #pragma unroll 1
@@ -649,14 +668,14 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                     tmem_st32(tOb + ch * 32u, ov);
                 }
             }
-            float2* const den = dens + ((items - 1) & 1u) * 512u + (uint32_t)row;
+            float2* const den = dens + (item & 1u) * 512u + (uint32_t)row;
             if (flags & (kCsPre | kCsLast)) den[grp * 128u] = make_float2(l, m);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(BAR(C_P_FULL0 + pair));
             if (!(flags & kCsLast)) continue;
             // Epilogue: the item's last P V. The other groups' shares were written before the P that it waited for.
-            if (!wait_bounded_warp(BAR(C_PV_DONE0 + pair), par, lim)) break;
+            if (!cs_wait(BAR(C_PV_DONE0 + pair), par, lim)) break;
             tc_fence_after();
             l += den[(grp ^ 1u) * 128u].x;
             if (!(flags & kCsFirst)) {
