@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 __all__ = ["LosaShape", "LosaError", "make_shape", "losa_dense_profile", "losa_select", "losa_select_noalloc",
            "losa_select_topk", "losa_sparse_attn",
@@ -48,6 +49,9 @@ class LosaRope(ctypes.Structure):
 class LosaCache(ctypes.Structure):
     _fields_ = [("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
                 ("n_pages", ctypes.c_int32), ("seqs", ctypes.c_int32), ("table_stride", ctypes.c_int32)]
+
+
+_token_view = struct.Struct("4i4q")  # LosaTokenView's layout
 
 
 class LosaTokenView(ctypes.Structure):
@@ -98,8 +102,8 @@ def load():
     L.losa_select_workspace_bytes.argtypes = [sp]
     L.losa_select_workspace_bytes.restype = sz
     L.losa_sparse_attn.argtypes = [sp, vp, vp, vp, f32, vp, vp, vp, vp, vp, vp]
-    rp, cp, tp = ctypes.POINTER(LosaRope), ctypes.POINTER(LosaCache), ctypes.POINTER(LosaTokenView)
-    L.losa_rope_apply.argtypes = [rp, i32, tp, vp, tp, vp, ctypes.c_uint32, i32, vp, vp, vp]
+    rp, cp = ctypes.POINTER(LosaRope), ctypes.POINTER(LosaCache)
+    L.losa_rope_apply.argtypes = [rp, i32, vp, vp, vp, vp, ctypes.c_uint32, i32, vp, vp, vp]  # views as packed bytes
     L.losa_cache_append.argtypes = [cp, rp, i32, vp, i64, i64, vp, i64, i64, i64, i32] + [vp] * 10
     L.losa_cache_attn.argtypes = ([cp, i32, i32, i32, vp, i64, i64, i64] + [vp] * 6 + [f32, i32, vp, i64, i64, i64] +
                                   [vp, vp, sz, vp])
@@ -178,7 +182,7 @@ def _ptrs(*specs):
         name = next(s[1] for s in specs if s[0] is not None and not isinstance(s[0], int) and s[0].get_device() < 0)
         raise ValueError(f"{name}: expected a CUDA tensor")
     if where:
-        here = torch.cuda.current_device()
+        here = torch._C._cuda_getDevice()
         if where.count(here) != len(where):
             t, name = next(s[:2] for s in specs
                            if s[0] is not None and not isinstance(s[0], int) and s[0].get_device() != here)
@@ -188,8 +192,8 @@ def _ptrs(*specs):
 
 def _stream(stream):
     if stream is None:
-        torch = _torch()
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        c = _torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -324,10 +328,9 @@ def losa_rope_apply(rope, x, y, rotate=1, inverse=False, positions=None, start=N
     xn, yn = x.shape, y.shape
     px, py, pp, ps = _ptrs((x, "x", dt, -5), (y, "y", dt, -5), (positions, "positions", "int32", 3 * xn[1] * xn[2]),
                            (start, "start", "int32", xn[1]))
-    xv = LosaTokenView(*xn[:4], *x.stride()[:4])
-    yv = LosaTokenView(*yn[:4], *y.stride()[:4])
-    st = load().losa_rope_apply(ctypes.byref(rope), code, ctypes.byref(xv), px, ctypes.byref(yv), py, int(rotate),
-                                int(bool(inverse)), pp, ps, _stream(stream))
+    st = load().losa_rope_apply(ctypes.byref(rope), code, _token_view.pack(*xn[:4], *x.stride()[:4]), px,
+                                _token_view.pack(*yn[:4], *y.stride()[:4]), py, int(rotate), int(bool(inverse)), pp, ps,
+                                _stream(stream))
     return _check(st, "losa_rope_apply", raise_on_error)
 
 
