@@ -3,13 +3,13 @@
 Every function has the name of its C entry point, takes torch CUDA tensors (or raw device pointers as ints)
 and passes their pointers, sizes and the current CUDA stream to the library. All computation happens in the
 library's CUDA kernels; there is no fallback. Importing this module does not load the library; the first call
-does, and raises if liblosa.so is missing (build it with `python -m free_block_sparse_losa_b200.build`).
+does, and raises if liblosa.so is missing (build it with `python -m free_block_sparse_losa_b200.build`). The streaming
+calls go through a compiled binding (_binding.so, same build): their checks and marshalling are the same, in C++.
 """
 from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 __all__ = ["LosaShape", "LosaError", "make_shape", "losa_dense_profile", "losa_select", "losa_select_noalloc",
            "losa_select_topk", "losa_sparse_attn",
@@ -49,9 +49,6 @@ class LosaRope(ctypes.Structure):
 class LosaCache(ctypes.Structure):
     _fields_ = [("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
                 ("n_pages", ctypes.c_int32), ("seqs", ctypes.c_int32), ("table_stride", ctypes.c_int32)]
-
-
-_token_view = struct.Struct("4i4q")  # LosaTokenView's layout
 
 
 class LosaTokenView(ctypes.Structure):
@@ -103,7 +100,8 @@ def load():
     L.losa_select_workspace_bytes.restype = sz
     L.losa_sparse_attn.argtypes = [sp, vp, vp, vp, f32, vp, vp, vp, vp, vp, vp]
     rp, cp = ctypes.POINTER(LosaRope), ctypes.POINTER(LosaCache)
-    L.losa_rope_apply.argtypes = [rp, i32, vp, vp, vp, vp, ctypes.c_uint32, i32, vp, vp, vp]  # views as packed bytes
+    tp = ctypes.POINTER(LosaTokenView)
+    L.losa_rope_apply.argtypes = [rp, i32, tp, vp, tp, vp, ctypes.c_uint32, i32, vp, vp, vp]
     L.losa_cache_append.argtypes = [cp, rp, i32, vp, i64, i64, vp, i64, i64, i64, i32] + [vp] * 10
     L.losa_cache_attn.argtypes = ([cp, i32, i32, i32, vp, i64, i64, i64] + [vp] * 6 + [f32, i32, vp, i64, i64, i64] +
                                   [vp, vp, sz, vp])
@@ -146,7 +144,7 @@ def _torch():
     global _torch_module
     if _torch_module is None:
         import torch
-        _dtypes.update({n: getattr(torch, n) for n in ("float32", "bfloat16", "int32", "float8_e4m3fn")})
+        _dtypes.update({n: getattr(torch, n) for n in ("float32", "bfloat16", "int32")})
         _torch_module = torch
     return _torch_module
 
@@ -155,9 +153,8 @@ def _ptrs(*specs):
     """Device pointers of arguments given as (value, name, dtype, numel). None stays NULL and an int is taken as a raw
     device pointer (the caller vouches for its size). A tensor must have the expected dtype (if given), hold at least
     `numel` elements (if given), be contiguous and live on the current CUDA device, so that a wrong buffer is refused
-    here instead of being read or written out of bounds on the GPU. A negative numel -n asks for n dimensions with any
-    strides but a contiguous last one instead. The dtype, size and layout of every argument are checked before any
-    argument's device."""
+    here instead of being read or written out of bounds on the GPU. The dtype, size and layout of every argument are
+    checked before any argument's device."""
     torch = _torch()
     out, where = [], []
     for t, name, dtype, numel in specs:
@@ -166,16 +163,10 @@ def _ptrs(*specs):
             continue
         if dtype is not None and t.dtype is not _dtypes[dtype]:
             raise ValueError(f"{name}: expected torch.{dtype}, got {t.dtype}")
-        if numel is not None and numel < 0:
-            if t.dim() != -numel:
-                raise ValueError(f"{name}: expected {-numel} dimensions, got {t.dim()}")
-            if t.stride(-1) != 1 and t.shape[-1] > 1:
-                raise ValueError(f"{name}: the last dimension must be contiguous")
-        else:
-            if numel is not None and t.numel() < numel:
-                raise ValueError(f"{name}: holds {t.numel()} elements, the shape needs {numel}")
-            if not t.is_contiguous():
-                raise ValueError(f"{name}: expected a contiguous tensor")
+        if numel is not None and t.numel() < numel:
+            raise ValueError(f"{name}: holds {t.numel()} elements, the shape needs {numel}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous tensor")
         where.append(t.get_device())  # -1 on the host
         out.append(t.data_ptr())
     if where and min(where) < 0:
@@ -310,57 +301,39 @@ def losa_sparse_attn(shape, q, k, v, scale, indptr, kv_block_idx, order, o, lse=
     return _check(st, "losa_sparse_attn", raise_on_error)
 
 
-def _float_dtype(t, name):
-    if t.dtype is _torch().bfloat16:
-        return "bfloat16", DTYPE_BF16
-    if t.dtype is _torch().float32:
-        return "float32", DTYPE_F32
-    raise ValueError(f"{name}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
+_binding = None
+
+
+def _fast():
+    """The streaming calls' argument marshalling (csrc/binding.cpp), bound to the loaded library."""
+    global _binding
+    if _binding is None:
+        import importlib
+        lib = load()
+        _torch()
+        try:
+            mod = importlib.import_module("._binding", __name__)
+        except ImportError as e:
+            raise RuntimeError(f"binding not built: {e} (python -m free_block_sparse_losa_b200.build)") from e
+        mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                   for f in ("losa_rope_apply", "losa_cache_append", "losa_cache_attn", "losa_cache_sparse_attn")))
+        _binding = mod
+    return _binding
 
 
 def losa_rope_apply(rope, x, y, rotate=1, inverse=False, positions=None, start=None, stream=None, raise_on_error=True):
     """x, y: (parts, batch, tokens, heads, head_dim) views of any layouts (last dimension contiguous); y may hold more
     tokens, which become zero rows. `rotate` is a bit mask of the parts that are rotated."""
-    dt, code = _float_dtype(x, "x")
-    if x.dim() != 5 or y.dim() != 5 or x.shape[4] != rope.head_dim or y.shape[4] != rope.head_dim:
-        raise ValueError(f"x, y: shapes {tuple(x.shape)}, {tuple(y.shape)}, expected (parts, batch, tokens, heads, "
-                         f"{rope.head_dim})")
-    xn, yn = x.shape, y.shape
-    px, py, pp, ps = _ptrs((x, "x", dt, -5), (y, "y", dt, -5), (positions, "positions", "int32", 3 * xn[1] * xn[2]),
-                           (start, "start", "int32", xn[1]))
-    st = load().losa_rope_apply(ctypes.byref(rope), code, _token_view.pack(*xn[:4], *x.stride()[:4]), px,
-                                _token_view.pack(*yn[:4], *y.stride()[:4]), py, int(rotate), int(bool(inverse)), pp, ps,
-                                _stream(stream))
-    return _check(st, "losa_rope_apply", raise_on_error)
-
-
-def _pool(cache, k8, v8, k_scale, v_scale, page_table, lens):
-    """_ptrs specs of a cache's buffers."""
-    n = max(cache.n_pages, 0) * max(cache.kv_heads, 0)
-    codes = n * max(cache.page_tokens, 0) * max(cache.head_dim, 0)
-    seqs = max(cache.seqs, 0)
-    return ((k8, "k8", "float8_e4m3fn", codes), (v8, "v8", "float8_e4m3fn", codes),
-            (k_scale, "k_scale", "float32", n), (v_scale, "v_scale", "float32", n),
-            (page_table, "page_table", "int32", seqs * max(cache.table_stride, 0)), (lens, "lens", "int32", seqs))
+    st = (_binding or _fast()).rope_apply(rope, x, y, rotate, inverse, positions, start, stream)
+    return st if st == 0 else _check(st, "losa_rope_apply", raise_on_error)
 
 
 def losa_cache_append(cache, k, v, k8, v8, k_scale, v_scale, page_table, lens, new_tokens, indptr=None, new_lens=None,
                       rope=None, positions=None, stream=None, raise_on_error=True):
     """k, v: (tokens, kv_heads, head_dim) of all sequences' new tokens, strided alike or not."""
-    dt, code = _float_dtype(k, "k")
-    n = k.shape[0]
-    if tuple(k.shape) != (n, cache.kv_heads, cache.head_dim) or v.shape != k.shape:
-        raise ValueError(f"k, v: shapes {tuple(k.shape)}, {tuple(v.shape)}, expected (tokens, {cache.kv_heads}, "
-                         f"{cache.head_dim}) of both")
-    p8, pv8, pks, pvs, pt, pl, pk, pv, pi, pn, pp = _ptrs(
-        *_pool(cache, k8, v8, k_scale, v_scale, page_table, lens), (k, "k", dt, -3), (v, "v", dt, -3),
-        (indptr, "indptr", "int32", cache.seqs + 1), (new_lens, "new_lens", "int32", cache.seqs),
-        (positions, "positions", "int32", 3 * n))
-    ks, vs = k.stride(), v.stride()
-    st = load().losa_cache_append(ctypes.byref(cache), None if rope is None else ctypes.byref(rope), code, pk, ks[0], ks[1],
-                                  pv, vs[0], vs[1], n, int(new_tokens), pi, pp, pt, pl, pn, p8, pv8, pks, pvs,
-                                  _stream(stream))
-    return _check(st, "losa_cache_append", raise_on_error)
+    st = (_binding or _fast()).cache_append(cache, k, v, k8, v8, k_scale, v_scale, page_table, lens, new_tokens, indptr,
+                                            new_lens, rope, positions, stream)
+    return st if st == 0 else _check(st, "losa_cache_append", raise_on_error)
 
 
 def losa_cache_attn_workspace_bytes(cache, heads, tokens, max_len=0) -> int:
@@ -371,34 +344,17 @@ def losa_cache_attn(cache, q, k8, v8, k_scale, v_scale, page_table, lens, scale,
                     workspace=None, stream=None, raise_on_error=True):
     """q, o: (seqs, tokens, heads, head_dim) bf16, any strides but a contiguous last dimension; lse: (seqs, tokens,
     heads). max_len bounds the lengths (0: the page table's capacity)."""
-    if q.dim() != 4:
-        raise ValueError(f"q: expected 4 dimensions, got {q.dim()}")
-    seqs, tokens, heads, d = q.shape
-    if seqs != cache.seqs or d != cache.head_dim or o.shape != q.shape:
-        raise ValueError(f"q, o: shapes {tuple(q.shape)}, {tuple(o.shape)}, expected ({cache.seqs}, tokens, heads, "
-                         f"{cache.head_dim}) of both")
-    p8, pv8, pks, pvs, pt, pl, pq, po, pe, pw = _ptrs(
-        *_pool(cache, k8, v8, k_scale, v_scale, page_table, lens), (q, "q", "bfloat16", -4), (o, "o", "bfloat16", -4),
-        (lse, "lse", "float32", seqs * tokens * heads), (workspace, "workspace", None, None))
-    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    qs, os_ = q.stride(), o.stride()
-    st = load().losa_cache_attn(ctypes.byref(cache), heads, tokens, int(bool(causal)), pq, qs[0], qs[1], qs[2],
-                                pt, pl, p8, pv8, pks, pvs, float(scale), int(max_len), po, os_[0], os_[1], os_[2], pe, pw,
-                                wsb, _stream(stream))
-    return _check(st, "losa_cache_attn", raise_on_error)
+    st = (_binding or _fast()).cache_attn(cache, q, k8, v8, k_scale, v_scale, page_table, lens, scale, o, lse, causal,
+                                          max_len, workspace, stream)
+    return st if st == 0 else _check(st, "losa_cache_attn", raise_on_error)
 
 
 def losa_cache_sparse_attn(shape, cache, q, k8, v8, k_scale, v_scale, page_table, lens, scale, o, indptr=None,
                            kv_block_idx=None, order=None, lse=None, stream=None, raise_on_error=True):
     """losa_sparse_attn over the paged 8-bit cache; without lists every block of the sequence is attended to."""
-    H, Np, d, nq, _ = _dims(shape)
-    p8, pv8, pks, pvs, pt, pl, pq, pi, px, pr, po, pe = _ptrs(
-        *_pool(cache, k8, v8, k_scale, v_scale, page_table, lens), (q, "q", "bfloat16", H * Np * d),
-        (indptr, "indptr", "int32", H * nq + 1), (kv_block_idx, "kv_block_idx", "int32", None),
-        (order, "order", "int32", H * nq), (o, "o", "bfloat16", H * Np * d), (lse, "lse", "float32", H * Np))
-    st = load().losa_cache_sparse_attn(ctypes.byref(shape), ctypes.byref(cache), pq, pt, pl, p8, pv8, pks, pvs,
-                                       float(scale), pi, px, pr, po, pe, _stream(stream))
-    return _check(st, "losa_cache_sparse_attn", raise_on_error)
+    st = (_binding or _fast()).cache_sparse_attn(shape, cache, q, k8, v8, k_scale, v_scale, page_table, lens, scale, o,
+                                                 indptr, kv_block_idx, order, lse, stream)
+    return st if st == 0 else _check(st, "losa_cache_sparse_attn", raise_on_error)
 
 
 def losa_get_device_error(stream=None) -> int:

@@ -1,4 +1,5 @@
-"""Build the CUDA library (liblosa.so) in-tree for sm_100a with nvcc."""
+"""Build the CUDA library (liblosa.so) for sm_100a with nvcc, and the Python side's argument marshalling (_binding.so) with
+the host compiler, in-tree."""
 from __future__ import annotations
 
 import glob
@@ -11,6 +12,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblosa.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 
 def nvcc() -> str:
@@ -37,8 +39,34 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = command(tmp, ("-Xptxas", "-v") if verbose else ())
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    build_binding()
     return LIB
+
+
+def binding_command(out: str = BINDING):
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    libs = [os.path.join(root, "lib")]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in includes],
+            os.path.join(CSRC, "binding.cpp"), "-o", out, *[f"-L{p}" for p in libs], "-ltorch_python", "-ltorch", "-ltorch_cpu",
+            "-lc10", "-lc10_cuda"]
+
+
+def build_binding(force: bool = False) -> str:
+    needs = [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "losa.h")]
+    if force or not os.path.exists(BINDING) or any(os.path.getmtime(s) > os.path.getmtime(BINDING) for s in needs):
+        tmp = BINDING + ".tmp"
+        subprocess.run(binding_command(tmp), check=True)
+        os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":
     print(build(force=True, verbose=True))
+    print(build_binding(force=True))
