@@ -417,15 +417,9 @@ __global__ void __launch_bounds__(kCsThreads, 1)
         // rows of a warp's step are ordered so that 16 lanes' 8-byte stores meet 16 different bank pairs.
         const uint32_t q4 = lane & 3u, r8 = (((lane >> 2) & 3u) << 1) | (lane >> 4);
         uint32_t items = 0;
-        for (uint32_t n = 0;; ++n) {
-            const CsTile* const rec = record(n);
-            if (!rec || rec->flags < 0) break;
-            const bool first = rec->flags & kCsFirst;
-            const int32_t qrow = rec->qrow;
-            release(n);
-            if (!first) continue;
+        auto split_q = [&](int32_t qrow) -> bool {
             const uint32_t qs = items & 1u;
-            if (!cs_wait(BAR(C_Q_EMPTY0 + qs), ((items >> 1) & 1u) ^ 1u, lim)) break;
+            if (!cs_wait(BAR(C_Q_EMPTY0 + qs), ((items >> 1) & 1u) ^ 1u, lim)) return false;
             const uint32_t dst = base + kCsQ + qs * 2 * kCsTile8;
 #pragma unroll 1
             for (uint32_t i = 0; i < 4; ++i) {
@@ -475,6 +469,19 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             fence_proxy_async_smem();
             mbar_arrive(BAR(C_Q_FULL0 + qs));
             ++items;
+            return true;
+        };
+        // The first item is known without its lists, pages and scales: its rows need not wait for the first records.
+        const int id0 = a.order ? a.order[blockIdx.x] : (int)blockIdx.x;
+        const bool early = id0 >= 0 && id0 < a.n_items;  // else the reader skips it
+        bool ok = !early || split_q((id0 / a.nq) * a.Np + id0 % a.nq * kTcRows);
+        for (uint32_t n = 0; ok; ++n) {
+            const CsTile* const rec = record(n);
+            if (!rec || rec->flags < 0) break;
+            const bool split = (rec->flags & kCsFirst) && !(early && rec->item == 0);
+            const int32_t qrow = rec->qrow;
+            release(n);
+            if (split) ok = split_q(qrow);
         }
     } else if (warp >= 20) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
@@ -543,8 +550,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             const uint32_t sl = (n + x) & 1u;
             if (fin[sl]) ok = flush(sl);
         }
-        if (warp == 20 && lane == 0) bulk_wait_all();
-        __syncwarp();
+        __syncwarp();  // flush has waited until the stores have read their slots; the grid's end waits for the rest
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 96;" ::: "memory");
         // ----------------------------------------------------------------------------- softmax warpgroups
