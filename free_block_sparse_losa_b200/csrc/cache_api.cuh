@@ -125,10 +125,11 @@ losa_status launch_append_width(int width, const AppendArgs& a, const void* k, c
                         : launch_append<T, D, 0>(a, k, v, grid, threads, stream);
 }
 
-// Where every sequence is short (max_len), or there is no more than one unit's worth of CTAs to gain, a CTA takes a unit and
-// there is nothing to join: up to 1024 keys the join would cost more than it saves (a warp then has eight tiles). Otherwise
-// two CTAs per SM share all units' keys in equal ranges; a unit, at most 1 / (kv heads x row tiles) of the work, lies in at
-// most CTAs / (kv heads x row tiles) + 2 of them, and in at most kCaMaxSplits (see ca_work).
+// Where every sequence is short (max_len), a CTA takes a unit and there is nothing to join: up to 1024 keys (12 kv heads, 1000
+// keys: 10.3 against 16.4 us), and up to 2048 where the units fill half the SMs by themselves (16 streams of 8 kv heads, 2000
+// keys: 15.7 against 18.5 us; with 32 units it is 15.4 against 14.4). Otherwise two CTAs per SM share all units' keys in equal
+// ranges; a unit, at most 1 / (kv heads x row tiles) of the work, lies in at most CTAs / (kv heads x row tiles) + 2 of
+// them, and in at most kCaMaxSplits (see ca_work).
 struct AttnPlan {
     int tile_rows, tiles, splits, ctas;
     int64_t rows;
@@ -147,7 +148,8 @@ AttnPlan attn_plan(const losa_cache* c, int heads, int tokens, int max_len, int 
     p.ml_bytes = p.total = 0;
     p.splits = 0;
     p.ctas = (int)(units * c->seqs);
-    if (len <= 1024 || units * c->seqs > (1 << 20)) return p;
+    const int64_t all = units * c->seqs;
+    if (len <= (2 * all >= sms ? 2048 : 1024) || all > (1 << 20)) return p;
     p.ctas = kCaCtas * sms;
     int64_t s = (p.ctas + units - 1) / units + 2;
     if (s > kCaMaxSplits) s = kCaMaxSplits;
@@ -161,15 +163,15 @@ bool attn_shape_ok(const losa_cache* c, int heads, int tokens) {
     return heads > 0 && heads % c->kv_heads == 0 && tokens > 0 && (int64_t)tokens * heads <= (1 << 24);
 }
 
-template <int D, int NB>
-losa_status launch_cache_attn(const losa_cache* c, CacheAttnArgs& a, const AttnPlan& p, const void* k8, const void* v8,
+template <int D, int NB, int NW>
+losa_status launch_cache_attn_warps(const losa_cache* c, CacheAttnArgs& a, const AttnPlan& p, const void* k8, const void* v8,
                               cudaStream_t stream) {
     CUtensorMap tk, tv;
     if (!make_code_map(&tk, c, k8, kCaKeys) || !make_code_map(&tv, c, v8, kCaKeys)) return LOSA_ERR_CUDA;
-    if (cudaFuncSetAttribute(cache_attn_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kCaSmem<D, NB>) != cudaSuccess)
+    if (cudaFuncSetAttribute(cache_attn_kernel<D, NB, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kCaSmem<D, NB, NW>) != cudaSuccess)
         return LOSA_ERR_CUDA;
-    cache_attn_kernel<D, NB><<<p.ctas, kCaWarps * 32, kCaSmem<D, NB>, stream>>>(tk, tv, a);
+    cache_attn_kernel<D, NB, NW><<<p.ctas, NW * 32, kCaSmem<D, NB, NW>, stream>>>(tk, tv, a);
     const losa_status st = launch_status();
     if (st != LOSA_OK || p.splits == 0) return st;
     // the join may be scheduled while the splits drain; it waits for their results itself
@@ -184,6 +186,14 @@ losa_status launch_cache_attn(const losa_cache* c, CacheAttnArgs& a, const AttnP
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, a, p.ctas) != cudaSuccess) return LOSA_ERR_CUDA;
     return launch_status();
+}
+
+// A CTA with a unit to itself and an SM to itself shares its tiles among more warps: a warp takes about 0.85 us for one.
+template <int D, int NB>
+losa_status launch_cache_attn(const losa_cache* c, CacheAttnArgs& a, const AttnPlan& p, const void* k8, const void* v8,
+                              int sms, cudaStream_t stream) {
+    return p.splits == 0 && p.ctas <= sms ? launch_cache_attn_warps<D, NB, kCaUnitWarps>(c, a, p, k8, v8, stream)
+                                          : launch_cache_attn_warps<D, NB, kCaWarps>(c, a, p, k8, v8, stream);
 }
 
 }  // namespace
@@ -369,10 +379,10 @@ losa_status losa_cache_attn(const losa_cache* cache, int32_t heads, int32_t toke
     a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.ml_bytes);
     a.wait_limit_ns = g_wait_limit_ns;
     if (p.tile_rows == kCaRows<1>)
-        return cache->head_dim == 128 ? launch_cache_attn<128, 1>(cache, a, p, k8, v8, stream)
-                                      : launch_cache_attn<64, 1>(cache, a, p, k8, v8, stream);
-    return cache->head_dim == 128 ? launch_cache_attn<128, 2>(cache, a, p, k8, v8, stream)
-                                  : launch_cache_attn<64, 2>(cache, a, p, k8, v8, stream);
+        return cache->head_dim == 128 ? launch_cache_attn<128, 1>(cache, a, p, k8, v8, sms, stream)
+                                      : launch_cache_attn<64, 1>(cache, a, p, k8, v8, sms, stream);
+    return cache->head_dim == 128 ? launch_cache_attn<128, 2>(cache, a, p, k8, v8, sms, stream)
+                                  : launch_cache_attn<64, 2>(cache, a, p, k8, v8, sms, stream);
 }
 
 losa_status losa_cache_sparse_attn(const losa_shape* shape, const losa_cache* cache, const void* q,

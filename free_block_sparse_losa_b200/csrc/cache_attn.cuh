@@ -20,7 +20,8 @@
 
 namespace losa {
 
-constexpr int kCaWarps = 4;
+constexpr int kCaWarps = 4;       // of a CTA that shares units with others
+constexpr int kCaUnitWarps = 8;   // of a CTA that has a short unit to itself
 constexpr int kCaKeys = 32;    // keys of a warp's tile: never more than one page
 constexpr int kCaMaxSplits = 128;
 constexpr float kCaBias = 10.0f;
@@ -145,8 +146,8 @@ template <int NB> constexpr int kCaRows = 8 * NB;
 // ragged streams of four rows, 95 against 92 us on two long ones of twelve.
 constexpr int kCaStages = 2;
 constexpr int kCaCtas = 2;
-template <int D, int NB> constexpr uint32_t kCaSmem =
-    kCaWarps * kCaStages * (2 * kCaTile<D> + 8) + kCaWarps * kCaRows<NB> * 8 + 1024;
+template <int D, int NB, int NW> constexpr uint32_t kCaSmem =
+    NW * kCaStages * (2 * kCaTile<D> + 8) + NW * kCaRows<NB> * 8 + 1024;
 
 // Reads the codes once and does little else: the memory rate bounds it, if enough warps share the latency of the
 // conversions and products in between. A warp owns a ring of 32-key tiles that TMA fills (one lane issues, one barrier per
@@ -155,8 +156,8 @@ template <int D, int NB> constexpr uint32_t kCaSmem =
 // usual orientation would leave half of 16 rows empty (92 against 87 us on eight ragged streams of four rows). P^T comes out of
 // S^T by movmatrix. The contraction is two orders of magnitude below the tensor peak here, and operands in registers need
 // no further copy through shared memory, which tcgen05 would.
-template <int D, int NB>
-__global__ void __launch_bounds__(kCaWarps * 32, kCaCtas)
+template <int D, int NB, int NW>
+__global__ void __launch_bounds__(NW * 32, kCaCtas * kCaWarps / NW)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CacheAttnArgs a) {
     constexpr int ROWS = kCaRows<NB>, STAGES = kCaStages;
@@ -169,13 +170,13 @@ __global__ void __launch_bounds__(kCaWarps * 32, kCaCtas)
     const uint32_t raw = smem_addr(ca_smem);
     uint8_t* const smem = ca_smem + (((raw + 1023u) & ~1023u) - raw);  // swizzled tiles need 1024-byte alignment
     const uint32_t base = smem_addr(smem);
-    constexpr uint32_t BARS = kCaWarps * STAGES * 2 * TILE;
+    constexpr uint32_t BARS = NW * STAGES * 2 * TILE;
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = lane_id();
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ring = base + warp * STAGES * 2 * TILE;
     const uint32_t bar = base + BARS + warp * STAGES * 8;
-    float2* const row_ml = reinterpret_cast<float2*>(smem + BARS + kCaWarps * STAGES * 8);
+    float2* const row_ml = reinterpret_cast<float2*>(smem + BARS + NW * STAGES * 8);
 
     const int C = a.g.page;
     const int units = a.g.kv_heads * a.tiles;
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(kCaWarps * 32, kCaCtas)
     const int tile = unit % a.tiles, kvh = unit / a.tiles;
     const int64_t unit_pos = seq_pos + (int64_t)unit * n_tiles;
     const int t0 = (int)(pos - unit_pos), t1 = n_tiles == 0 ? 0 : (int)min((int64_t)n_tiles, stop - unit_pos);
-    const int mine = max(0, (t1 - t0 - warp + kCaWarps - 1) / kCaWarps);  // this warp's tiles: t0 + warp, + 4, ...
+    const int mine = max(0, (t1 - t0 - warp + NW - 1) / NW);  // this warp's tiles: t0 + warp, + 4, ...
 
     // Raw query rows, row 8 nb + g of the tile: asked for before the copies of codes, which would hold them up.
     const int n_rows = a.tokens * a.group;
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(kCaWarps * 32, kCaCtas)
         const int i = j + (int)lane;
         at_row = -1;
         if (i < mine) {
-            const int key = (t0 + warp + i * kCaWarps) * kCaKeys, blk = key / C;
+            const int key = (t0 + warp + i * NW) * kCaKeys, blk = key / C;
             at_page = a.g.table[(int64_t)seq * a.g.table_stride + blk];
             if (at_page < 0 || at_page >= a.g.n_pages) atomicOr(&g_device_error, kDevErrBadData);
             else at_row = (int)(((int64_t)at_page * a.g.kv_heads + kvh) * C + (key - blk * C));
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kCaWarps * 32, kCaCtas)
         const float2 sc = make_float2(__shfl_sync(0xffffffffu, at_ks, j & 31),
                                       fmaxf(__shfl_sync(0xffffffffu, at_vs, j & 31), 1e-30f));
         const uint32_t tk = ring + s * 2 * TILE, tv = tk + TILE;
-        const int key0 = (t0 + warp + j * kCaWarps) * kCaKeys;
+        const int key0 = (t0 + warp + j * NW) * kCaKeys;
         const int have = sc.x < 0.0f ? 0 : min(kCaKeys, len - key0);  // keys of this tile that exist
         // S^T: 16 keys x 8 rows at a time; a lane's keys are 16 i + kg and 16 i + 8 + kg
         float sv[2][NB][4];
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kCaWarps * 32, kCaCtas)
         for (uint32_t x = base_fill + j; x != filled; ++x)
             wait_bounded_warp(bar + 8 * (x % STAGES), (x / STAGES) & 1u, kDrainLimitNs);
 
-    // Join the four warps through their own rings: [ROWS][D] fp32 each.
+    // Join the warps through their own rings: [ROWS][D] fp32 each.
     float* const mine_o = reinterpret_cast<float*>(smem + warp * STAGES * 2 * TILE);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -485,16 +486,16 @@ __global__ void __launch_bounds__(kCaWarps * 32, kCaCtas)
         }
     __syncthreads();
     const bool shared = a.splits != 0 && t1 - t0 < n_tiles;  // other CTAs hold the rest of the unit
-    for (int i = threadIdx.x; i < ROWS * (D / 4); i += kCaWarps * 32) {
+    for (int i = threadIdx.x; i < ROWS * (D / 4); i += NW * 32) {
         const int r = i / (D / 4), d0 = (i - r * (D / 4)) * 4;
         const int row = tile * ROWS + r;
         if (row >= n_rows) continue;
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kCaWarps; ++w) top = fmaxf(top, row_ml[w * ROWS + r].x);
+        for (int w = 0; w < NW; ++w) top = fmaxf(top, row_ml[w * ROWS + r].x);
         float den = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int w = 0; w < kCaWarps; ++w) {
+        for (int w = 0; w < NW; ++w) {
             const float2 ml = row_ml[w * ROWS + r];
             const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - top);
             const float4 v = *reinterpret_cast<const float4*>(smem + w * STAGES * 2 * TILE + (r * D + d0) * 4);
