@@ -46,13 +46,22 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Four values as codes, the first in the low byte.
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+// Four values times s as codes, the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, uint64_t s) {
     uint32_t r;
-    asm("{\n\t.reg .b16 l, h;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .b64 x, y;\n\t.reg .f32 p, q, u, v;\n\t"
+        "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+        "mul.rn.f32x2 x, x, %5;\n\tmul.rn.f32x2 y, y, %5;\n\t"
+        "mov.b64 {p, q}, x;\n\tmov.b64 {u, v}, y;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 l, q, p;\n\tcvt.rn.satfinite.e4m3x2.f32 h, v, u;\n\t"
         "mov.b32 %0, {l, h};\n\t}"
-        : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+        : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d), "l"(s));
+    return r;
+}
+// The largest magnitude of three (NaN is passed over).
+__device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 __device__ __forceinline__ uint32_t e4m3x2_of_half2(uint32_t h) {
@@ -212,7 +221,8 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, const T* __rest
 #pragma unroll
             for (int s = 0; s < SIDES; ++s)
 #pragma unroll
-                for (int e = 0; e < N; ++e) top = fmaxf(top, fabsf(f[p][s][e]));
+                for (int e = 0; e + 1 < N; e += 2) top = fmax3_abs(top, f[p][s][e], f[p][s][e + 1]);
+            if (N == 1) top = fmax3_abs(top, f[p][0][0], f[p][SIDES - 1][0]);
         }
         uint32_t* const buf = part[h & 1];
         auto block_max = [&](float x) -> uint32_t {  // of non-negative numbers, as bits
@@ -263,7 +273,9 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, const T* __rest
             __syncthreads();  // every thread has read the old scale
         }
         if (threadIdx.x == 0) scale[at] = sc;
-        const float inv = 1.0f / sc;
+        // a fresh scale's reciprocal is another power of two
+        const float inv = lo > 0 ? 1.0f / sc : __uint_as_float((254u << 23) - __float_as_uint(sc));
+        const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             if (!real[p]) continue;
@@ -273,10 +285,9 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, const T* __rest
                 const float (&g)[N] = f[p][s];
                 if constexpr (N == 8) {
                     *reinterpret_cast<uint2*>(out) =
-                        make_uint2(e4m3x4(g[0] * inv, g[1] * inv, g[2] * inv, g[3] * inv),
-                                   e4m3x4(g[4] * inv, g[5] * inv, g[6] * inv, g[7] * inv));
+                        make_uint2(e4m3x4(g[0], g[1], g[2], g[3], inv2), e4m3x4(g[4], g[5], g[6], g[7], inv2));
                 } else if constexpr (N == 4) {
-                    *reinterpret_cast<uint32_t*>(out) = e4m3x4(g[0] * inv, g[1] * inv, g[2] * inv, g[3] * inv);
+                    *reinterpret_cast<uint32_t*>(out) = e4m3x4(g[0], g[1], g[2], g[3], inv2);
                 } else if constexpr (N == 2) {
                     *reinterpret_cast<uint16_t*>(out) = (uint16_t)e4m3x2(g[0] * inv, g[1] * inv);
                 } else {
