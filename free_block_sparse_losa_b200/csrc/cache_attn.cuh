@@ -87,9 +87,8 @@ __device__ __forceinline__ float row_factor(uint32_t amax_bits) {
 
 // The work of a call. A unit is a (sequence, kv head, row tile); its work is its sequence's 32-key tiles. The units' tiles,
 // one behind the other, are cut into equal ranges, one per CTA, across the units' borders: ragged lengths and any number of
-// heads load every SM alike (cutting each sequence by itself left a third of the time idle: 127 against 83 us on eight
-// ragged streams). A unit that lies in several ranges is joined by cache_join_kernel. Every CTA finds its place in the
-// lengths by itself.
+// heads load every SM alike (cutting each sequence by itself: 110 against 94 us on eight ragged streams). A unit that lies
+// in several ranges is joined by cache_join_kernel. Every CTA finds its place in the lengths by itself.
 struct CaWork {
     int64_t total, range;  // tiles of the call; of a CTA
 };
@@ -128,7 +127,7 @@ __device__ __forceinline__ CaWork ca_work(const CacheAttnArgs& a, int ctas, int 
     CaWork w;
     w.total = sum * units;
     w.range = ca_div(w.total + ctas - 1, ctas);
-    // at least eight tiles for each warp pair of loads to pay, and no unit in more than `splits` ranges
+    // at least two tiles a warp, and no unit in more than `splits` ranges
     const int least = (most + a.splits - 3) / (a.splits - 2);  // splits > 2
     w.range = max(w.range, (int64_t)max(least, 2 * kCaWarps));
     return w;
