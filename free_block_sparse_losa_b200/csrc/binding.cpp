@@ -196,6 +196,16 @@ Pool pool_of(Args& a, const losa_cache* c, PyObject* const* o) {  // k8, v8, k_s
     return p;
 }
 
+// The C call itself runs without the interpreter's lock, as one by ctypes does: a launch may wait for room in its queue, and
+// other threads go on meanwhile. Its arguments are read before.
+template <typename F> losa_status unlocked(F call) {
+    losa_status st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = call();
+    Py_END_ALLOW_THREADS;
+    return st;
+}
+
 // Runs f, turning what it throws into a Python error; returns the status as an int.
 template <typename F> PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F f) {
     if (got != want) {
@@ -236,7 +246,11 @@ PyObject* rope_apply(PyObject*, PyObject* const* o, Py_ssize_t n) {
                     t.stride(0), t.stride(1), t.stride(2), t.stride(3)};
         }
         const uint32_t rotate = (uint32_t)whole(o[3]);
-        return g_rope_apply(rope.get(), code_of(type), &v[0], px, &v[1], py, rotate, truth(o[4]), pos, start, stream_of(o[7]));
+        const bool inverse = truth(o[4]);
+        cudaStream_t stream = stream_of(o[7]);
+        return unlocked([&] {
+            return g_rope_apply(rope.get(), code_of(type), &v[0], px, &v[1], py, rotate, inverse, pos, start, stream);
+        });
     });
 }
 
@@ -259,9 +273,14 @@ PyObject* cache_append(PyObject*, PyObject* const* o, Py_ssize_t n) {
         int32_t* new_lens = (int32_t*)a.buffer(o[11], "new_lens", at::kInt, seqs);
         const int32_t* pos = (const int32_t*)a.buffer(o[13], "positions", at::kInt, 3 * k.size(0));
         a.check_devices();
-        return g_cache_append(cache.get(), rope.get(), code_of(type), pk, k.stride(0), k.stride(1), pv, v.stride(0),
-                              v.stride(1), k.size(0), int32_of(o[9], "new_tokens"), indptr, pos, p.table, p.lens, new_lens,
-                              p.k8, p.v8, p.k_scale, p.v_scale, stream_of(o[14]));
+        const int64_t ks[2] = {k.stride(0), k.stride(1)}, vs[2] = {v.stride(0), v.stride(1)}, total = k.size(0);
+        const int32_t new_tokens = int32_of(o[9], "new_tokens");
+        cudaStream_t stream = stream_of(o[14]);
+        return unlocked([&] {
+            return g_cache_append(cache.get(), rope.get(), code_of(type), pk, ks[0], ks[1], pv, vs[0], vs[1], total,
+                                  new_tokens, indptr, pos, p.table, p.lens, new_lens, p.k8, p.v8, p.k_scale, p.v_scale,
+                                  stream);
+        });
     });
 }
 
@@ -285,10 +304,16 @@ PyObject* cache_attn(PyObject*, PyObject* const* o, Py_ssize_t n) {
             ws_bytes = (size_t)w.numel() * w.element_size();
         }
         a.check_devices();
-        return g_cache_attn(cache.get(), extent(q.size(2), "q"), extent(q.size(1), "q"), truth(o[11]), pq, q.stride(0),
-                            q.stride(1), q.stride(2), p.table, p.lens, p.k8, p.v8, p.k_scale, p.v_scale, real(o[8]),
-                            int32_of(o[12], "max_len"), po, out.stride(0), out.stride(1), out.stride(2), lse, ws, ws_bytes,
-                            stream_of(o[14]));
+        const int32_t heads = extent(q.size(2), "q"), tokens = extent(q.size(1), "q"), causal = truth(o[11]);
+        const int64_t qs[3] = {q.stride(0), q.stride(1), q.stride(2)};
+        const int64_t os[3] = {out.stride(0), out.stride(1), out.stride(2)};
+        const float scale = real(o[8]);
+        const int32_t max_len = int32_of(o[12], "max_len");
+        cudaStream_t stream = stream_of(o[14]);
+        return unlocked([&] {
+            return g_cache_attn(cache.get(), heads, tokens, causal, pq, qs[0], qs[1], qs[2], p.table, p.lens, p.k8, p.v8,
+                                p.k_scale, p.v_scale, scale, max_len, po, os[0], os[1], os[2], lse, ws, ws_bytes, stream);
+        });
     });
 }
 
@@ -310,8 +335,12 @@ PyObject* cache_sparse_attn(PyObject*, PyObject* const* o, Py_ssize_t n) {
         void* out = a.buffer(o[10], "o", at::kBFloat16, tokens);
         float* lse = (float*)a.buffer(o[14], "lse", at::kFloat, rows);
         a.check_devices();
-        return g_cache_sparse_attn(shape.get(), cache.get(), q, p.table, p.lens, p.k8, p.v8, p.k_scale, p.v_scale, real(o[9]),
-                                   indptr, idx, order, out, lse, stream_of(o[15]));
+        const float scale = real(o[9]);
+        cudaStream_t stream = stream_of(o[15]);
+        return unlocked([&] {
+            return g_cache_sparse_attn(shape.get(), cache.get(), q, p.table, p.lens, p.k8, p.v8, p.k_scale, p.v_scale, scale,
+                                       indptr, idx, order, out, lse, stream);
+        });
     });
 }
 

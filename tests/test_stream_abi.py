@@ -1,6 +1,9 @@
 """CPU checks of the streaming entry points: host-side refusals before anything is launched, and the binding's checks of
 tensors. No call here reaches the CUDA runtime."""
 import ctypes
+import subprocess
+import threading
+import time
 
 import pytest
 import torch
@@ -180,3 +183,34 @@ def test_binding_refuses_wrong_tensors(lib):
     with pytest.raises(ValueError, match="o: holds"):
         L.losa_cache_sparse_attn(L.make_shape(4, 100, 128, 128, 128, 32, "bf16"), c, t(4, 128, 128), *pool(), 0.1,
                                  t(4, 127, 128))
+
+
+def test_calls_leave_the_interpreter_to_other_threads(lib, tmp_path):
+    """A launch may wait for room in its queue: other Python threads go on meanwhile, as during a ctypes call. A C function
+    that takes its time stands in for the entry points; with raw pointers no argument needs a device."""
+    src = tmp_path / "slow.c"
+    src.write_text("#include <unistd.h>\nint slow(void) { usleep(400000); return 0; }\n")
+    subprocess.run(["gcc", "-shared", "-fPIC", str(src), "-o", str(tmp_path / "slow.so")], check=True)
+    slow = ctypes.cast(ctypes.CDLL(str(tmp_path / "slow.so")).slow, ctypes.c_void_p).value
+    mod = L._fast()
+    mod.bind(slow, slow, slow, slow)
+    try:
+        shape, c = L.make_shape(16, 200, 256, 128, 128, 32, "bf16"), L.make_cache(2, 128, 32, 6, 2, 3)
+        laps, done = [], threading.Event()
+
+        def other():
+            while not done.is_set():
+                laps.append(time.perf_counter())
+                time.sleep(0.001)
+
+        t = threading.Thread(target=other)
+        t.start()
+        begin = time.perf_counter()
+        assert L.losa_cache_sparse_attn(shape, c, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0.1, 2 * FAKE, stream=0) == 0
+        end = time.perf_counter()
+        done.set()
+        t.join()
+        assert sum(begin + 0.05 < x < end - 0.05 for x in laps) >= 5
+    finally:
+        L._binding = None
+        L._fast()
