@@ -124,7 +124,6 @@ class KvCache:
         self._lens = torch.zeros((2, seqs), dtype=torch.int32, device=device)
         self._now = 0
         self.max_len = 0
-        self._workspace = torch.empty(16, dtype=torch.uint8, device=device)
 
     @property
     def lens(self):
@@ -143,12 +142,16 @@ class KvCache:
         self.max_len = min(self.max_len + int(new_tokens), self.cache.table_stride * self.page_tokens)
 
     def attend(self, q, scale, o, lse=None, causal=True, stream=None):
-        """The last tokens q (seqs, tokens, heads, d), appended before, over the whole cache."""
+        """The last tokens q (seqs, tokens, heads, d), appended before, over the whole cache. The workspace comes from the
+        allocator on the call's stream every time: calls on several streams, and captured ones, each have their own."""
         need = losa_cache_attn_workspace_bytes(self.cache, q.shape[2], q.shape[1], self.max_len)
-        if need > self._workspace.numel():
-            self._workspace = torch.empty(need, dtype=torch.uint8, device=self.k8.device)
+        workspace = None
+        if need:
+            where = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+            with torch.cuda.stream(where):  # None: the current one
+                workspace = torch.empty(need, dtype=torch.uint8, device=self.k8.device)
         losa_cache_attn(self.cache, q, *self.buffers, self.lens, scale, o, lse=lse, causal=causal, max_len=self.max_len,
-                        workspace=self._workspace, stream=stream)
+                        workspace=workspace, stream=stream)
 
     def sparse(self, layer, q, scale, out, lse=None, lists=True, order=True, stream=None):
         """Query blocks of a layer (LayerBuffers with block_k = page_tokens) over its frozen lists, or over every block."""

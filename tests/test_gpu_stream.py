@@ -733,6 +733,43 @@ def test_captured_steps_replayed_on_new_inputs():
 
 
 @pytest.mark.gpu
+def test_a_captured_decode_keeps_its_workspace():
+    """A decode captured through the harness shares no memory with later calls: calls with other row counts, and tensors made
+    since, are as they were after a replay; and calls on two streams at once give what one gives."""
+    require_gpu()
+    from free_block_sparse_losa_b200.harness import KvCache
+    g = gen(57)
+    hk, d, n = 2, 128, 6000
+    cache = KvCache(2, hk, d, n, page_tokens=64)
+    cache.append(*torch.randn(2, 2 * n, hk, d, generator=g, device="cuda").bfloat16(), n)
+    q = [torch.randn(2, t, 8, d, generator=g, device="cuda").bfloat16() for t in (1, 1, 3)]
+    o = [torch.zeros_like(x) for x in q]
+    for x, y in zip(q, o):
+        cache.attend(x, 0.05, y)
+    want = [y.clone() for y in o]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.attend(q[0], 0.05, o[0])
+    cache.attend(q[2], 0.05, o[2])
+    need = L.losa_cache_attn_workspace_bytes(cache.cache, 8, 1, n)
+    assert need > 0
+    marks = [torch.full((need + 7 * i,), 90 + i, dtype=torch.uint8, device="cuda") for i in range(8)]
+    for y in o:
+        y.zero_()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(streams[0]):
+            graph.replay()
+        cache.attend(q[1], 0.05, o[1], stream=streams[1])
+        cache.attend(q[2], 0.05, o[2], stream=torch.cuda.default_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, w) for y, w in zip(o, want))
+    assert all(bool((m == 90 + i).all()) for i, m in enumerate(marks))
+    assert L.losa_get_device_error() == 0
+
+
+@pytest.mark.gpu
 def test_offsets_beyond_32_bits():
     """A pool of more than 2^31 codes and a rotation of more than 2^31 elements: the far ends are read and written."""
     require_gpu()
