@@ -28,12 +28,16 @@
 // TMEM: S_0 0..127, S_1 128..255, O 256..383, P_0 384..447, P_1 448..511. An S buffer is free once its pair has it in
 // registers, so Q K^T runs two tiles ahead of P V.
 //
-// Measured on a 4680-token chunk over 32760 keys (12 heads) and on a 480p layer with 16 listed 32-key blocks a row: 1052 and
-// 198 us, 906 and 521 TFLOP/s. Steps that brought it there: one softmax path, keys that do not exist as -inf, and V widened
+// Measured on a 4680-token chunk over 32760 keys (12 heads) and on a 480p layer with 16 listed 32-key blocks a row: 990 and
+// 193 us, 963 and 535 TFLOP/s. Steps that brought it there: one softmax path, keys that do not exist as -inf, and V widened
 // without register swaps (1523 -> 1175 us, 297 -> 252); groups that take tiles in turn instead of halving every tile
-// (-> 1141); MMA issued from uniform registers, four groups and Q split by warps of its own (-> 1052, 259 -> 198). Leaving
-// out half of the MMAs, the exponentials or the widening takes at most a tenth off: no single unit bounds it, but the chain
-// S -> maximum -> weights -> P of two tiles in flight. Three groups of whole rows with P over S are slower (1175, 214 us).
+// (-> 1141); MMA issued from uniform registers, four groups and Q split by warps of its own (-> 1052, 259 -> 198); waits for
+// two barriers at once, a pair that walks only its own tiles, the first rows split before their records (-> 990, 193). Leaving
+// out half of the MMAs, the exponentials or the widening takes at most a tenth off, all three a fifth: no single unit bounds
+// it, but the chain S -> maximum -> weights -> P of two tiles in flight, and with short lists 3 us an item. Slower: three
+// groups of whole rows with P over S (1175, 214 us), rows whole in a warp by 16-lane TMEM loads (7 %), O written behind the
+// next tile's maximum (a fifth; registers). No faster: warps of their own for each product, blocks taken from the grid as
+// CTAs come free.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>

@@ -142,8 +142,9 @@ template <typename T, int N> struct Pack {
 // Every row is read once and written once; nothing else moves, so the kernel is bound by memory. A thread owns one unit of
 // one token and walks that token's (part, head) rows with the unit's cosines and sines in registers: the angles are computed
 // once per token instead of once per row, which would cost more than the copy. Measured: a 480p projection (12 heads, query,
-// key and value, 604 MB) in 103 us, 5.9 TB/s; the 720p gradient (24 heads, query and key, 2.9 GB) in 447 us, 6.5 TB/s. Loads
-// that mark their lines for early eviction cost 3 % of that, rows by two or eight at a time 4 to 8 %.
+// key and value, 604 MB) in 102 us, 5.9 TB/s; the 720p gradient (24 heads, query and key, 2.9 GB) in 447 us, 6.5 TB/s, on two
+// sets of tensors in turn, in 483 on three. Loads that mark their lines for early eviction cost 3 % of that, rows by two or
+// eight at a time 4 to 8 %.
 template <typename T, int W>
 __global__ void __launch_bounds__(kRopeThreads) rope_apply_kernel(const __grid_constant__ RopeApplyArgs a,
                                                                   const T* __restrict__ x, T* __restrict__ y) {
