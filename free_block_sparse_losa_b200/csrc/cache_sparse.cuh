@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
             tmem_ld32(tSb, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
             tmem_ld32(tSb + 32u, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
             // the row's factor was written before Q K^T could start
-            const float c = fmaxf(a.scale_log2 * fac[(item & 3u) * 128u + (uint32_t)row], 1e-37f);
+            const float c = a.scale_log2 * fac[(item & 3u) * 128u + (uint32_t)row];
             tmem_wait_ld();
             tc_fence_before();
             mbar_arrive(BAR(C_S_FREE0 + pair));
@@ -618,7 +618,10 @@ __global__ void __launch_bounds__(kCsThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) mx[e] = fmax3(mx[e], z[y + e], z[y + 4 + e]);
                 const float q = fmaxf(fmax3(mx[0], mx[1], fmaxf(z[28], z[29])), fmax3(mx[2], mx[3], fmaxf(z[30], z[31])));
+                // at least the smallest normal number: -inf times a factor that rounds to zero (a quiet row on a block of
+                // zero keys, whose scale is 2^-40) would be NaN
                 ck[x] *= c;
+                ck[x] = ck[x] < 1.17549435e-38f ? 1.17549435e-38f : ck[x];
                 top = fmaxf(top, fmaf(q, ck[x], lv[x]));
             }
             // The tile before first, then this one: a pair that published a tile before it had seen the other's could run

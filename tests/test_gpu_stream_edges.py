@@ -1,0 +1,74 @@
+"""The streaming calls at the ends of what their documentation allows, against 64-bit forms; the tolerances are those of
+tests/test_gpu_stream.py unless a test derives its own."""
+import math
+
+import pytest
+import torch
+
+import free_block_sparse_losa_b200 as L
+from tests.gpu_util import require_gpu
+from tests.test_gpu_stream import attend, attn_close, check_blocks, dense, gen, poisoned_cache
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def blocks_call(q, pool, table, lens, page, heads, hk, n, scale, **lists):
+    """The blocked call over the cache of poisoned_cache; returns o and lse."""
+    H, rows, d = q.shape
+    o, lse = torch.full_like(q, 9.0), torch.full((H, rows), 9.0, device="cuda")
+    cache = L.make_cache(hk, d, page, pool[0].shape[0], table.shape[0], table.shape[1])
+    L.losa_cache_sparse_attn(L.make_shape(H, n, rows, d, 128, page, "bf16"), cache, q, *pool, table, ints(lens), scale, o,
+                             lse=lse, **lists)
+    return o, lse
+
+
+def decode_call(q, pool, table, lens, scale, causal=True, max_len=0):
+    """The few-token call over the cache of poisoned_cache; returns o and lse."""
+    seqs, tokens, heads, d = q.shape
+    hk, page = pool[0].shape[1:3]
+    cache = L.make_cache(hk, d, page, pool[0].shape[0], seqs, table.shape[1])
+    ws = torch.empty(max(16, L.losa_cache_attn_workspace_bytes(cache, heads, tokens, max_len)), dtype=torch.uint8,
+                     device="cuda")
+    o, lse = torch.full_like(q, 9.0), torch.full((seqs, tokens, heads), 9.0, device="cuda")
+    L.losa_cache_attn(cache, q, *pool, table, ints(lens), scale, o, lse=lse, causal=causal, max_len=max_len, workspace=ws)
+    return o, lse
+
+
+def check_decode(q, o, lse, pool, table, lens, scale, causal=True):
+    seqs, tokens, heads, d = q.shape
+    k8, v8, ks, vs = pool
+    hk = k8.shape[1]
+    G = heads // hk
+    for b in range(seqs):
+        end = torch.arange(tokens, device="cuda").repeat_interleave(G)
+        end = lens[b] - (tokens - 1 - end) if causal else torch.full_like(end, lens[b])
+        for h in range(hk):
+            at = slice(h * G, (h + 1) * G)
+            want, wl, size = attend(q[b, :, at].double().reshape(-1, d), dense(k8, ks, table, b, h, lens[b]),
+                                    dense(v8, vs, table, b, h, lens[b]), end, scale)
+            attn_close(o[b, :, at].reshape(-1, d), lse[b, :, at].reshape(-1), want, wl, size)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page,n", [(32, 70), (128, 200), (64, 1000)])
+def test_blocks_of_zero_keys_and_quiet_rows(page, n):
+    """Blocks of zero keys carry the smallest scale, 2^-40; times the factor of a row whose largest element is near 2^-110
+    that is zero in fp32. A part-full last block of them must still hide the slots that hold no token."""
+    require_gpu()
+    g = gen(61)
+    width = -(-n // page)
+    k8, v8, ks, vs, table = poisoned_cache(g, [n], 1, page, 128, width)
+    used = table[0].long()
+    slot = torch.arange(width * page, device="cuda").view(width, 1, page) < n
+    codes = k8.view(torch.uint8)
+    codes[used] = torch.where(slot[..., None], 0, codes[used])
+    ks[used] = 2.0 ** -40
+    q = torch.randn(1, 128, 128, generator=g, device="cuda").bfloat16()
+    q[0, ::3] *= 2.0 ** -110
+    q[0, 1::3] *= 2.0 ** -120
+    for scale in (0.09, 1e-6):
+        o, lse = blocks_call(q, (k8, v8, ks, vs), table, [n], page, 1, 1, 128, scale)
+        assert L.losa_get_device_error() == 0
+        check_blocks(q, o, lse, (k8, v8, ks, vs), table, [n], page, 1, 1, 128, scale, None, None)
