@@ -239,18 +239,21 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                                 if (w_id < 0 || w_id >= a.n_items) {
                                     bad = 1;
                                     w_id = -2;  // not an item: skipped
-                                } else if (a.indptr) {
-                                    w_begin = a.indptr[w_id];
-                                    w_count = a.indptr[w_id + 1] - w_begin;
-                                    if (w_count < 0 || w_begin < 0) {
-                                        bad = 1;
-                                        w_count = 0;
-                                    }
                                 } else {
-                                    const int64_t len = a.g.lens[w_id / a.nq / a.heads];
-                                    w_begin = 0;
-                                    w_count = (int)min((int64_t)a.g.table_stride,
-                                                       max(len, (int64_t)0) / a.g.page + (max(len, (int64_t)0) % a.g.page != 0));
+                                    // reported here: an item without entries has no tile that would look at its length
+                                    const int len = a.g.lens[w_id / a.nq / a.heads], room = a.g.table_stride * a.g.page;
+                                    if (len < 0 || len > room) bad = 1;
+                                    if (a.indptr) {
+                                        w_begin = a.indptr[w_id];
+                                        w_count = a.indptr[w_id + 1] - w_begin;
+                                        if (w_count < 0 || w_begin < 0) {
+                                            bad = 1;
+                                            w_count = 0;
+                                        }
+                                    } else {
+                                        w_begin = 0;
+                                        w_count = (min(max(len, 0), room) + a.g.page - 1) / a.g.page;
+                                    }
                                 }
                             }
                         }
@@ -288,11 +291,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 if (q_flags >= 0 && e < q_count) {
                     const int off = (g & (4 / a.sub - 1)) * 32;
                     const int j = a.indptr ? a.kv_idx[q_begin + e] : e;
-                    int64_t len = a.g.lens[seq];
-                    if (len < 0 || len > (int64_t)a.g.table_stride * a.g.page) {
-                        bad = 1;
-                        len = len < 0 ? 0 : (int64_t)a.g.table_stride * a.g.page;
-                    }
+                    const int64_t len = min(max(a.g.lens[seq], 0), a.g.table_stride * a.g.page);
                     if (j < 0 || j >= a.g.table_stride) {
                         bad = 1;
                     } else {

@@ -72,3 +72,27 @@ def test_blocks_of_zero_keys_and_quiet_rows(page, n):
         o, lse = blocks_call(q, (k8, v8, ks, vs), table, [n], page, 1, 1, 128, scale)
         assert L.losa_get_device_error() == 0
         check_blocks(q, o, lse, (k8, v8, ks, vs), table, [n], page, 1, 1, 128, scale, None, None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lists", [None, "empty", "some"])
+@pytest.mark.parametrize("lens,clamped", [([-1, 200], [0, 200]), ([200, 257], [200, 256]), ([200, -2 ** 31], [200, 0])])
+def test_blocks_report_every_bad_length(lists, lens, clamped):
+    """A length out of [0, capacity] is reported whether or not a list entry looks at it, and read as the nearest end."""
+    require_gpu()
+    g = gen(62)
+    page, heads, n = 64, 2, 200
+    k8, v8, ks, vs, table = poisoned_cache(g, [256, 256], 1, page, 128, 4)
+    q = torch.randn(2 * heads, 256, 128, generator=g, device="cuda").bfloat16()
+    items = 2 * heads * 2
+    counts = {None: None, "empty": [0] * items, "some": [0, 2] * (items // 2)}[lists]
+    kw = {}
+    if counts:
+        kw = dict(indptr=ints([sum(counts[:i]) for i in range(items + 1)]), kv_block_idx=ints([0, 3] * max(1, sum(counts) // 2)))
+    o, lse = blocks_call(q, (k8, v8, ks, vs), table, lens, page, heads, 1, n, 0.02, **kw)
+    assert L.losa_get_device_error() == -5
+    check_blocks(q, o, lse, (k8, v8, ks, vs), table, clamped, page, heads, 1, n, 0.02, kw.get("indptr"),
+                 kw.get("kv_block_idx"))
+    good = blocks_call(q, (k8, v8, ks, vs), table, clamped, page, heads, 1, n, 0.02, **kw)
+    assert L.losa_get_device_error() == 0
+    assert torch.equal(good[0], o) and torch.equal(good[1], lse)
