@@ -79,9 +79,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return r;
 }
 
-// The power of two that brings a row's largest finite magnitude (its bits) into [2^7, 2^8); 1 for a zero row.
+// The power of two that brings a row's largest magnitude (its bits) into [2^7, 2^8); 1 for a zero row. A row with an infinity
+// or NaN has no softmax: its factor is NaN, which makes every element of the row NaN, and so o and lse where it sees a key.
 __device__ __forceinline__ float row_factor(uint32_t amax_bits) {
     const int e = (int)(amax_bits >> 23);
+    if (e == 255) return __uint_as_float(0x7fffffffu);
     return e == 0 ? 1.0f : __uint_as_float((uint32_t)min(max(127 + 127 + 7 - e, 1), 254) << 23);
 }
 
@@ -299,8 +301,7 @@ __global__ void __launch_bounds__(NW * 32, kCaCtas * kCaWarps / NW)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const uint32_t u = x ? w[s].y : w[s].x;
-                const uint32_t lo = (u & 0x7fffu) << 16, hi = u & 0x7fff0000u;
-                amax = max(amax, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
+                amax = max(amax, max((u & 0x7fffu) << 16, u & 0x7fff0000u));
             }
         }
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
@@ -511,11 +512,12 @@ __global__ void __launch_bounds__(NW * 32, kCaCtas * kCaWarps / NW)
             *reinterpret_cast<float4*>(a.part_o + at * D + d0) = make_float4(o[0], o[1], o[2], o[3]);
             if (d0 == 0) a.part_ml[at] = make_float2(top, den);
         } else {
-            const float inv = top == -INFINITY ? 0.0f : 1.0f / den;
+            // zero only where no key was seen: a row of NaN has a maximum of -inf as well
+            const float inv = den == 0.0f ? 0.0f : 1.0f / den;
             *reinterpret_cast<uint2*>(a.o + seq * a.o_seq + token * a.o_token + head * a.o_head + d0) =
                 make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
             if (a.lse && d0 == 0)
-                a.lse[id] = top == -INFINITY ? -INFINITY : (top - kCaBias + __log2f(den)) * 0.6931471805599453f;
+                a.lse[id] = den == 0.0f ? -INFINITY : (top - kCaBias + __log2f(den)) * 0.6931471805599453f;
         }
     }
     pos += max(t1 - t0, 1);
@@ -571,14 +573,14 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
     den = (dens[0] + dens[1]) + (dens[2] + dens[3]);
     if (threadIdx.x < D / 2) {
         const int d = 2 * threadIdx.x;
-        const float inv = top == -INFINITY ? 0.0f : 1.0f / den;
+        const float inv = den == 0.0f ? 0.0f : 1.0f / den;
         const float u = (sum[0][d] + sum[1][d]) + (sum[2][d] + sum[3][d]);
         const float v = (sum[0][d + 1] + sum[1][d + 1]) + (sum[2][d + 1] + sum[3][d + 1]);
         *reinterpret_cast<uint32_t*>(a.o + seq * a.o_seq + token * a.o_token + head * a.o_head + d) =
             pack_bf16x2(u * inv, v * inv);
     }
     if (a.lse && threadIdx.x == 0)
-        a.lse[id] = top == -INFINITY ? -INFINITY : (top - kCaBias + __log2f(den)) * 0.6931471805599453f;
+        a.lse[id] = den == 0.0f ? -INFINITY : (top - kCaBias + __log2f(den)) * 0.6931471805599453f;
 }
 
 }  // namespace losa

@@ -467,7 +467,8 @@ __global__ void __launch_bounds__(kCsThreads, 1)
                 }
                 // four items deep: item k's slot is written again for item k + 4, whose split waits for Q K^T of item
                 // k + 2, which waited until item k's last S had been read
-                if (q4 == 0) fac[(items & 3u) * 128u + row] = 1.0f / s;
+                // (of a row of NaN 1: hidden keys must stay -inf)
+                if (q4 == 0) fac[(items & 3u) * 128u + row] = s == s ? 1.0f / s : 1.0f;
             }
             fence_proxy_async_smem();
             mbar_arrive(BAR(C_Q_FULL0 + qs));

@@ -276,7 +276,8 @@ losa_status losa_cache_append(const losa_cache* cache, const losa_rope* rope, in
  *   lse       : [seqs][tokens][heads] fp32 or NULL.
  *   workspace : scratch of losa_cache_attn_workspace_bytes(cache, heads, tokens, max_len) bytes, 16-byte aligned (may be
  *               NULL where that is 0), used during the call only; calls that can overlap need their own.
- * A row that sees no key (an empty sequence) gets o = 0 and lse = -inf. Logits, weights' sums and O are fp32; weights
+ * A row that sees no key (an empty sequence) gets o = 0 and lse = -inf. A row with an infinity or NaN in q gets NaN in o and
+ * lse where it sees a key, whatever the signs of the codes. Logits, weights' sums and O are fp32; weights
  * are rounded to fp16 for the product with V. Codes of slots that hold no token are never used, whatever they are. A length
  * outside [0, capacity] or a page out of range sets the device error word (LOSA_ERR_DEVICE_FAULT); the keys concerned
  * are left out.
@@ -299,7 +300,8 @@ losa_status losa_cache_attn(const losa_cache* cache, int32_t heads, int32_t toke
  *               indptr's last entry: the library cannot check that.
  *   order     : work order, or NULL, as for losa_sparse_attn.
  *   scale     : logit scale, > 0.
- * A row that sees no key (an empty list, an empty sequence) gets o = 0 and lse = -inf. Query elements below 2^-9 of their
+ * A row that sees no key (an empty list, an empty sequence) gets o = 0 and lse = -inf; one with an infinity or NaN in q gets
+ * NaN in both where it sees a key. Query elements below 2^-9 of their
  * row's largest are off by at most 2^-17 of it; weights are rounded to fp16 for the product with V; the rest is fp32. Codes of
  * slots that hold no token are never used. A block, page, length, offset or work-order entry out of range sets the device
  * error word (LOSA_ERR_DEVICE_FAULT); the blocks concerned are left out.

@@ -96,3 +96,58 @@ def test_blocks_report_every_bad_length(lists, lens, clamped):
     good = blocks_call(q, (k8, v8, ks, vs), table, clamped, page, heads, 1, n, 0.02, **kw)
     assert L.losa_get_device_error() == 0
     assert torch.equal(good[0], o) and torch.equal(good[1], lse)
+
+
+BAD = (math.inf, -math.inf, math.nan)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,lens,tokens,max_len", [(128, [1, 40, 0], 1, 64), (64, [700, 3], 2, 64), (128, [5000, 1, 0], 1, 0),
+                                                   (64, [3000, 2500], 5, 0)])
+def test_decode_rows_with_infinities_are_nan(d, lens, tokens, max_len):
+    """A query row that holds an infinity or NaN has no softmax: o and lse are NaN wherever it sees a key, however the keys'
+    signs fall, and zero and -inf where it sees none. Other rows keep their bits."""
+    require_gpu()
+    g = gen(64)
+    seqs, hk, heads, page = len(lens), 2, 6, 32
+    width = -(-max(lens) // page)
+    *pool, table = poisoned_cache(g, lens, hk, page, d, width)
+    q = torch.randn(seqs, tokens, heads, d, generator=g, device="cuda").bfloat16()
+    clean = decode_call(q, pool, table, lens, 0.1, max_len=max_len)
+    bad = torch.zeros(seqs, tokens, heads, dtype=torch.bool, device="cuda")
+    for i, (h, value) in enumerate(zip((0, 3, 4), BAD)):
+        q[:, :, h, (7 * i + 5) % d] = value
+        bad[:, :, h] = True
+    o, lse = decode_call(q, pool, table, lens, 0.1, max_len=max_len)
+    assert L.losa_get_device_error() == 0
+    end = ints(lens)[:, None] - (tokens - 1 - torch.arange(tokens, device="cuda"))
+    nan = bad & (end > 0)[:, :, None]
+    assert bool(o[nan].isnan().all()) and bool(lse[nan].isnan().all())
+    assert torch.equal(o[~nan], clean[0][~nan]) and torch.equal(lse[~nan], clean[1][~nan])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page,lens,listed", [(128, [300, 0], False), (32, [1, 999], False), (64, [500, 130], True)])
+def test_block_rows_with_infinities_are_nan(page, lens, listed):
+    """The same of the blocked call."""
+    require_gpu()
+    g = gen(65)
+    heads, n, seqs = 2, 200, len(lens)
+    width = -(-max(lens) // page)
+    *pool, table = poisoned_cache(g, lens, 1, page, 128, width)
+    q = torch.randn(seqs * heads, 256, 128, generator=g, device="cuda").bfloat16()
+    kw, sees = {}, ints(lens).repeat_interleave(2 * heads) > 0
+    if listed:
+        counts = [0, 3, 1, 2] * seqs
+        kw = dict(indptr=ints([sum(counts[:i]) for i in range(len(counts) + 1)]), kv_block_idx=ints([0, 1, 2, 1, 0, 2] * seqs))
+        sees = ints(counts) > 0
+    clean = blocks_call(q, pool, table, lens, page, heads, 1, n, 0.1, **kw)
+    bad = torch.zeros(seqs * heads, 256, dtype=torch.bool, device="cuda")
+    for i, value in enumerate(BAD):
+        q[:, 17 * i + 1::64, 31 * i] = value
+        bad[:, 17 * i + 1::64] = True
+    o, lse = blocks_call(q, pool, table, lens, page, heads, 1, n, 0.1, **kw)
+    assert L.losa_get_device_error() == 0
+    nan = bad & sees.view(seqs * heads, 2).repeat_interleave(128, 1)
+    assert bool(o[nan].isnan().all()) and bool(lse[nan].isnan().all())
+    assert torch.equal(o[~nan], clean[0][~nan]) and torch.equal(lse[~nan], clean[1][~nan])
