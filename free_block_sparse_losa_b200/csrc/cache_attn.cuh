@@ -79,12 +79,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return r;
 }
 
-// The power of two that brings a row's largest magnitude (its bits) into [2^7, 2^8); 1 for a zero row. A row with an infinity
-// or NaN has no softmax: its factor is NaN, which makes every element of the row NaN, and so o and lse where it sees a key.
+// The power of two that brings a row's largest magnitude (its bits) into [2^7, 2^8), or as near as 2^127 brings it
+// (subnormal numbers below 2). A row with an infinity or NaN has no softmax: its factor is NaN, which makes every element of
+// the row NaN, and so o and lse where it sees a key.
 __device__ __forceinline__ float row_factor(uint32_t amax_bits) {
     const int e = (int)(amax_bits >> 23);
     if (e == 255) return __uint_as_float(0x7fffffffu);
-    return e == 0 ? 1.0f : __uint_as_float((uint32_t)min(max(127 + 127 + 7 - e, 1), 254) << 23);
+    return __uint_as_float((uint32_t)min(max(127 + 127 + 7 - e, 1), 254) << 23);
 }
 
 // The work of a call. A unit is a (sequence, kv head, row tile); its work is its sequence's 32-key tiles. The units' tiles,

@@ -151,3 +151,50 @@ def test_block_rows_with_infinities_are_nan(page, lens, listed):
     nan = bad & sees.view(seqs * heads, 2).repeat_interleave(128, 1)
     assert bool(o[nan].isnan().all()) and bool(lse[nan].isnan().all())
     assert torch.equal(o[~nan], clean[0][~nan]) and torch.equal(lse[~nan], clean[1][~nan])
+
+
+def subnormal_rows(q):
+    """q's values as bf16 numbers below 2^-126, of the same signs."""
+    bits = (q.float().abs() * 40).clamp(max=127).to(torch.int16)
+    return torch.where(q < 0, bits | -2 ** 15, bits).view(torch.bfloat16)
+
+
+# (scale, sizes of rows): logits of the loudest rows are near one, the others' near zero
+ROWS = [(0.03 * 2.0 ** -40, (40, 0, -50, None, 38)), (0.03 * 2.0 ** -100, (100, 96, 0, None)), (0.03 * 2.0 ** 60, (-60, -64, -110, None)),
+        (0.03 * 2.0 ** 100, (-100, -103, None)), (2.0 ** 124, ("sub", None, "sub"))]
+
+
+def sized(q, sizes):
+    """Rows of q (leading dimensions flattened) brought to the sizes in turn: a power of two, None for zeros."""
+    rows = q.view(-1, q.shape[-1])
+    for i, s in enumerate(sizes):
+        part = rows[i::len(sizes)]
+        rows[i::len(sizes)] = subnormal_rows(part) if s == "sub" else torch.zeros_like(part) if s is None else part * 2.0 ** s
+    return q
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale,sizes", ROWS)
+@pytest.mark.parametrize("d,tokens,max_len", [(128, 1, 64), (64, 4, 0)])
+def test_decode_rows_of_any_size(scale, sizes, d, tokens, max_len):
+    require_gpu()
+    g = gen(68)
+    lens, hk, heads, page = [1300, 77], 1, 5, 64
+    *pool, table = poisoned_cache(g, lens, hk, page, d, -(-max(lens) // page))
+    q = sized(torch.randn(2, tokens, heads, d, generator=g, device="cuda").bfloat16(), sizes)
+    o, lse = decode_call(q, pool, table, lens, scale, max_len=max_len)
+    assert L.losa_get_device_error() == 0
+    check_decode(q, o, lse, pool, table, lens, scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale,sizes", ROWS)
+def test_block_rows_of_any_size(scale, sizes):
+    require_gpu()
+    g = gen(69)
+    lens, page, heads, n = [900], 64, 2, 256
+    *pool, table = poisoned_cache(g, lens, 1, page, 128, -(-max(lens) // page))
+    q = sized(torch.randn(heads, n, 128, generator=g, device="cuda").bfloat16(), sizes)
+    o, lse = blocks_call(q, pool, table, lens, page, heads, 1, n, scale)
+    assert L.losa_get_device_error() == 0
+    check_blocks(q, o, lse, pool, table, lens, page, heads, 1, n, scale, None, None)
