@@ -357,6 +357,7 @@ losa_status losa_cache_attn(const losa_cache* cache, int32_t heads, int32_t toke
     a.g = cache_geom(cache, page_table, lens);
     a.k_scale = k_scale;
     a.v_scale = v_scale;
+    a.v8 = static_cast<const uint8_t*>(v8);
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.o = static_cast<__nv_bfloat16*>(o);
     a.lse = lse;

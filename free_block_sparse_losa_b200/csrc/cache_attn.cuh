@@ -30,6 +30,7 @@ struct CacheAttnArgs {
     CacheGeom g;
     const float* k_scale;
     const float* v_scale;
+    const uint8_t* v8;
     const __nv_bfloat16* q;
     __nv_bfloat16* o;
     float* lse;                // [seqs][tokens][heads] or null
@@ -60,6 +61,14 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
     uint2 r;
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr));
     return r;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+    return r;
+}
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -336,7 +345,7 @@ __global__ void __launch_bounds__(NW * 32, kCaCtas * kCaWarps / NW)
     }
     const int ka = key_of_column(2 * t), kb = key_of_column(2 * t + 1), kg = key_of_column(g);
 
-    bool ok = true;
+    bool ok = true, veiled_nan = false;
     int j = 0;
     for (; j < mine; ++j) {
         const uint32_t f = base_fill + j, s = f % STAGES;
@@ -346,6 +355,21 @@ __global__ void __launch_bounds__(NW * 32, kCaCtas * kCaWarps / NW)
         const uint32_t tk = ring + s * 2 * TILE, tv = tk + TILE;
         const int key0 = (t0 + warp + j * NW) * kCaKeys;
         const int have = sc.x < 0.0f ? 0 : min(kCaKeys, len - key0);  // keys of this tile that exist
+        if (key0 + have > least) {
+            // Some keys are hidden from some rows, whose weight 0 must not meet a NaN in V: it becomes 0 here, and the rows
+            // that see it get it behind the loop. (Given to them at once it costs 3 % of a long call in scheduling.)
+            bool found = false;
+            for (uint32_t at = tv + max(least - key0, 0) * D + 4 * lane; at < tv + have * D; at += 128) {
+                const uint32_t w = ld_shared_u32(at), nan = __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                if (nan) {
+                    st_shared_u32(at, w & ~nan);
+                    found = true;
+                }
+            }
+            veiled_nan |= __any_sync(0xffffffffu, found) != 0;
+            fence_proxy_async_smem();  // a copy writes the tile next
+            __syncwarp();
+        }
         // S^T: 16 keys x 8 rows at a time; a lane's keys are 16 i + kg and 16 i + 8 + kg
         float sv[2][NB][4];
 #pragma unroll
@@ -485,6 +509,22 @@ __global__ void __launch_bounds__(NW * 32, kCaCtas * kCaWarps / NW)
             for (int n = 0; n < MT; ++n)
                 *reinterpret_cast<float2*>(mine_o + r * D + VD * g + 2 * n) = make_float2(acc[n][nb][x], acc[n][nb][2 + x]);
         }
+    if (veiled_nan) {  // NaN codes of keys that some rows do not see, for the rows that do
+        __syncwarp();
+        for (int i = max(0, (least / kCaKeys - t0 - warp) / NW); i < mine; ++i) {
+            const int key0 = (t0 + warp + i * NW) * kCaKeys;
+            for (int key = max(key0, least); key < min(key0 + kCaKeys, len); ++key) {
+                const int page = a.g.table[(int64_t)seq * a.g.table_stride + key / C];
+                if (page < 0 || page >= a.g.n_pages) continue;
+                const uint8_t* const v = a.v8 + (((int64_t)page * a.g.kv_heads + kvh) * C + key % C) * D;
+                for (int e = (int)lane; e < D; e += 32) {
+                    if ((v[e] & 0x7f) != 0x7f) continue;
+                    for (int r = 0; r < ROWS && tile * ROWS + r < n_rows; ++r)
+                        if (key < len - (a.tokens - 1 - (tile * ROWS + r) / a.group)) mine_o[r * D + e] = __uint_as_float(0x7fffffffu);
+                }
+            }
+        }
+    }
     __syncthreads();
     const bool shared = a.splits != 0 && t1 - t0 < n_tiles;  // other CTAs hold the rest of the unit
     for (int i = threadIdx.x; i < ROWS * (D / 4); i += NW * 32) {

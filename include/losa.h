@@ -267,7 +267,8 @@ losa_status losa_cache_append(const losa_cache* cache, const losa_rope* rope, in
 /*
  * Attention of the last `tokens` tokens of every sequence over its whole cache (their own keys included: append first).
  *   heads     : query heads, a multiple of kv_heads; query head h reads kv head h / (heads / kv_heads).
- *   causal    : non-zero: token i of the `tokens` sees keys 0 .. lens[b] - tokens + i; zero: every key.
+ *   causal    : non-zero: token i of the `tokens` sees keys 0 .. lens[b] - tokens + i; zero: every key. What a key that a
+ *               row does not see holds, NaN too, does not reach the row.
  *   q, o      : bf16, element (b, i, h, e) at b seq_stride + i token_stride + h head_stride + e; strides are multiples of 8
  *               elements. o must not overlap q.
  *   scale     : logit scale, > 0.

@@ -198,3 +198,36 @@ def test_block_rows_of_any_size(scale, sizes):
     o, lse = blocks_call(q, pool, table, lens, page, heads, 1, n, scale)
     assert L.losa_get_device_error() == 0
     check_blocks(q, o, lse, pool, table, lens, page, heads, 1, n, scale, None, None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,lens,tokens,heads,max_len", [
+    (128, [33, 3, 64], 3, 2, 64), (64, [96, 2, 1], 5, 4, 64), (128, [4000, 1025], 4, 4, 0), (64, [2049, 4000], 8, 4, 0),
+    (128, [1500, 1499], 40, 2, 0)])
+def test_decode_hides_later_tokens_whatever_they_hold(d, lens, tokens, heads, max_len):
+    """NaN codes in the values or keys of a drafted token reach the rows that see it and no earlier one: a value's NaN in its
+    own dimension, a key's in the whole row."""
+    require_gpu()
+    g = gen(66)
+    page, hk, seqs = 32, 2, len(lens)
+    width = -(-max(lens) // page)
+    k8, v8, ks, vs, table = poisoned_cache(g, lens, hk, page, d, width)
+    q = torch.randn(seqs, tokens, heads, d, generator=g, device="cuda").bfloat16()
+    clean = decode_call(q, (k8, v8, ks, vs), table, lens, 0.1, max_len=max_len)
+    for keys in (False, True):
+        codes = [k8.clone(), v8.clone()]
+        want = torch.zeros_like(q, dtype=torch.bool)
+        for b, n in enumerate(lens):
+            for back, dim in ((0, 3), (0, d - 1), (1, 0), (tokens // 2, 37), (tokens - 1, 5)):
+                at = n - 1 - back  # a key that rows tokens - 1 - back and later see
+                if at < 0:
+                    continue
+                codes[0 if keys else 1].view(torch.uint8)[int(table[b, at // page]), :, at % page, dim] = 0x7F | (0x80 * (back & 1))
+                first = max(0, tokens - 1 - back)
+                want[b, first:, :, slice(None) if keys else dim] = True
+        o, lse = decode_call(q, (codes[0], codes[1], ks, vs), table, lens, 0.1, max_len=max_len)
+        assert L.losa_get_device_error() == 0
+        assert torch.equal(o.isnan(), want)
+        assert torch.equal(o[~want], clean[0][~want])
+        rows = want.all(-1)
+        assert torch.equal(lse.isnan(), rows) and torch.equal(lse[~rows], clean[1][~rows])
