@@ -28,7 +28,13 @@ struct RopePos {
     int p[3];
 };
 
-// Position of token n of the grid, or the caller's (t, y, x) triple.
+// The quotient rounded down; y > 0.
+__device__ __forceinline__ int floor_div(int x, int y) {
+    const int q = x / y;
+    return q - (x - q * y < 0 ? 1 : 0);
+}
+
+// Position of token n of the grid (negative: before its first), or the caller's (t, y, x) triple.
 __device__ __forceinline__ RopePos rope_position(const RopeArgs& r, const int32_t* triple, int n) {
     RopePos q;
     if (triple) {
@@ -36,7 +42,7 @@ __device__ __forceinline__ RopePos rope_position(const RopeArgs& r, const int32_
         q.p[1] = triple[1];
         q.p[2] = triple[2];
     } else {
-        const int row = n / r.gx, t = row / r.gy;
+        const int row = floor_div(n, r.gx), t = floor_div(row, r.gy);
         q.p[0] = t;
         q.p[1] = row - t * r.gy;
         q.p[2] = n - row * r.gx;

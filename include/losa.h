@@ -224,7 +224,8 @@ typedef struct {
  *   inverse   : non-zero turns by the negative angles: R is orthogonal, so this is the gradient of the forward call
  *               (with the two layouts exchanged), and with rotate = 0 the way back from head-major to token-major.
  *   positions : [batch][tokens][3] int32 (t, y, x), or NULL for the grid.
- *   start     : [batch] int32, the grid token that row 0 of a batch element is, or NULL for 0. Ignored with positions.
+ *   start     : [batch] int32, the grid token that row 0 of a batch element is, or NULL for 0 (negative: token -1 sits at
+ *               (-1, grid_y - 1, grid_x - 1)). Ignored with positions.
  */
 losa_status losa_rope_apply(const losa_rope* rope, int32_t dtype, const losa_token_view* x_view, const void* x,
                             const losa_token_view* y_view, void* y, uint32_t rotate, int32_t inverse,

@@ -231,3 +231,24 @@ def test_decode_hides_later_tokens_whatever_they_hold(d, lens, tokens, heads, ma
         assert torch.equal(o[~want], clean[0][~want])
         rows = want.all(-1)
         assert torch.equal(lse.isnan(), rows) and torch.equal(lse[~rows], clean[1][~rows])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rope_tokens_before_the_grid(dtype):
+    """A negative start is a token before the grid's first: the one before (0, 0, 0) is (-1, gy - 1, gx - 1), as explicit
+    positions say it."""
+    require_gpu()
+    g = gen(67)
+    gy, gx, n, d = 5, 7, 90, 64
+    x = torch.randn(1, 3, n, 2, d, generator=g, device="cuda").to(dtype)
+    starts = [-1, -36, -1000003]
+    a, b = torch.empty_like(x), torch.empty_like(x)
+    rope = L.make_rope(d, (16, 22, 18), (gy, gx))
+    L.losa_rope_apply(rope, x, a, start=ints(starts))
+    tok = ints(starts).long()[:, None] + torch.arange(n, device="cuda")
+    row = tok.div(gx, rounding_mode="floor")
+    pos = torch.stack([row.div(gy, rounding_mode="floor"), row.remainder(gy), tok.remainder(gx)], -1)
+    L.losa_rope_apply(rope, x, b, positions=pos.int().contiguous())
+    assert L.losa_get_device_error() == 0
+    assert torch.equal(a, b)
