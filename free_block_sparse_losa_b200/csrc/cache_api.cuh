@@ -267,8 +267,9 @@ losa_status losa_cache_append(const losa_cache* cache, const losa_rope* rope, in
         return LOSA_ERR_INVALID_ARG;
     const int size = dtype == LOSA_DTYPE_BF16 ? 2 : 4;
     const int64_t strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
-    for (int64_t s : strides)
-        if (s < 0 || (s * size) % 16 != 0) return LOSA_ERR_INVALID_ARG;
+    const int64_t counts[2] = {total_tokens, cache->kv_heads};
+    for (int i = 0; i < 4; ++i)  // nothing steps by the stride of an extent of one
+        if (counts[i % 2] > 1 && (strides[i] < 0 || (strides[i] * size) % 16 != 0)) return LOSA_ERR_INVALID_ARG;
     if (total_tokens > 0 && (!aligned16(k) || !aligned16(v))) return LOSA_ERR_INVALID_ARG;
     if (!aligned16(k8) || !aligned16(v8) || !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(page_table) ||
         !aligned4(lens) || lens == new_lens)

@@ -246,7 +246,7 @@ typedef struct {
  *   rope      : rotation of the keys, or NULL (keys are stored as they come). Without positions the token that becomes
  *               number n of its sequence sits at grid token n.
  *   dtype     : of k and v. Token i, head h of k starts at element i k_token_stride + h k_head_stride; likewise v. Strides
- *               are multiples of 16 bytes.
+ *               are multiples of 16 bytes; that of an extent of one does not matter.
  *   total_tokens : tokens that k and v hold. Sequence b's new tokens are rows indptr[b] .. indptr[b + 1) (int32
  *               [seqs + 1]), at most new_tokens of them, or, with indptr NULL, rows b new_tokens .. (b + 1) new_tokens.
  *   positions : [total_tokens][3] int32 (t, y, x), or NULL.

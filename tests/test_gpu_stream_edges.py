@@ -7,7 +7,7 @@ import torch
 
 import free_block_sparse_losa_b200 as L
 from tests.gpu_util import require_gpu
-from tests.test_gpu_stream import attend, attn_close, check_blocks, dense, gen, poisoned_cache
+from tests.test_gpu_stream import attend, attn_close, check_blocks, dense, gen, make_pool, poisoned_cache
 
 
 def ints(v):
@@ -252,3 +252,21 @@ def test_rope_tokens_before_the_grid(dtype):
     L.losa_rope_apply(rope, x, b, positions=pos.int().contiguous())
     assert L.losa_get_device_error() == 0
     assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_append_strides_of_single_extents():
+    """One kv head, and one token: the stride that nothing steps by may be anything."""
+    require_gpu()
+    g = gen(74)
+    d, page = 64, 32
+    for tokens, hk, strides in ((7, 1, (2 * d, 5)), (1, 3, (13, 2 * d)), (1, 1, (3, 1))):
+        base = torch.randn(2, 1000, generator=g, device="cuda").bfloat16()
+        kv = [b.as_strided((tokens, hk, d), (*strides, 1)) for b in base]
+        out = []
+        for k, v in (kv, [t.contiguous() for t in kv]):
+            pool = make_pool(gen(75), 2, hk, page, d)
+            L.losa_cache_append(L.make_cache(hk, d, page, 2, 1, 2), k, v, *pool, ints([[1, 0]]), ints([30]), tokens)
+            out.append(pool)
+        assert L.losa_get_device_error() == 0
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(*out))
