@@ -3,6 +3,7 @@ a layer's paged 8-bit key/value cache (KvCache) with PyTorch (device memory and 
 in order. No computation happens here; every step runs in the library's kernels."""
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 
 import numpy as np
@@ -25,6 +26,13 @@ def host_tokens_to_device(a: np.ndarray, dtype: str, device="cuda") -> torch.Ten
 
 def device_tokens_to_f32(t: torch.Tensor) -> np.ndarray:
     return t.float().cpu().numpy()
+
+
+def _on_stream(stream):
+    """Allocations and copies inside belong to a call on `stream` (None: the current one; an int: a raw handle)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 @dataclass
@@ -109,7 +117,10 @@ class LayerBuffers:
 
 class KvCache:
     """A layer's paged 8-bit cache for `seqs` sequences of up to `capacity` tokens: its pool, page table (each sequence's
-    pages in order) and lengths, which live on the device. max_len bounds the lengths on the host."""
+    pages in order) and lengths, which live on the device. An eager append leaves the lengths before it where they were and
+    flips to another buffer; from the first append captured into a graph on, `lens` is one tensor that every append advances,
+    eager or replayed, so that both go on from each other. max_len bounds the lengths on the host; as replays are not seen
+    there, it is the capacity from the first captured append on."""
 
     def __init__(self, seqs, kv_heads, head_dim, capacity, page_tokens=128, rope=None, device="cuda"):
         self.seqs, self.page_tokens, self.rope = seqs, page_tokens, rope
@@ -123,6 +134,7 @@ class KvCache:
         self.page_table = torch.arange(seqs * width, dtype=torch.int32, device=device).view(seqs, width)
         self._lens = torch.zeros((2, seqs), dtype=torch.int32, device=device)
         self._now = 0
+        self._captured = False
         self.max_len = 0
 
     @property
@@ -138,8 +150,14 @@ class KvCache:
         nxt = 1 - self._now
         losa_cache_append(self.cache, k, v, *self.buffers, self.lens, new_tokens, indptr=indptr, new_lens=self._lens[nxt],
                           rope=self.rope, positions=positions, stream=stream)
-        self._now = nxt
-        self.max_len = min(self.max_len + int(new_tokens), self.cache.table_stride * self.page_tokens)
+        capacity = self.cache.table_stride * self.page_tokens
+        with _on_stream(stream):
+            self._captured |= torch.cuda.is_current_stream_capturing()
+            if self._captured:
+                self.lens.copy_(self._lens[nxt])
+        if not self._captured:
+            self._now = nxt
+        self.max_len = capacity if self._captured else min(self.max_len + int(new_tokens), capacity)
 
     def attend(self, q, scale, o, lse=None, causal=True, stream=None):
         """The last tokens q (seqs, tokens, heads, d), appended before, over the whole cache. The workspace comes from the
@@ -147,8 +165,7 @@ class KvCache:
         need = losa_cache_attn_workspace_bytes(self.cache, q.shape[2], q.shape[1], self.max_len)
         workspace = None
         if need:
-            where = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-            with torch.cuda.stream(where):  # None: the current one
+            with _on_stream(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device=self.k8.device)
         losa_cache_attn(self.cache, q, *self.buffers, self.lens, scale, o, lse=lse, causal=causal, max_len=self.max_len,
                         workspace=workspace, stream=stream)

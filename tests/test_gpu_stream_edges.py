@@ -270,3 +270,56 @@ def test_append_strides_of_single_extents():
             out.append(pool)
         assert L.losa_get_device_error() == 0
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(*out))
+
+
+@pytest.mark.gpu
+def test_a_captured_harness_step_advances_with_every_replay():
+    """KvCache.append and attend captured once and replayed token by token, with eager calls before, between and behind: the
+    cache, its lengths and the outputs are what eager calls alone give."""
+    require_gpu()
+    from free_block_sparse_losa_b200.harness import KvCache
+    g = gen(63)
+    hk, d, heads, seqs = 2, 64, 4, 2
+    rope = L.make_rope(d, (20, 22, 20), (3, 5))
+    start = torch.randn(2, seqs * 50, hk, d, generator=g, device="cuda").bfloat16()
+    steps = torch.randn(9, 2, seqs, hk, d, generator=g, device="cuda").bfloat16()
+    qs = torch.randn(9, seqs, 1, heads, d, generator=g, device="cuda").bfloat16()
+
+    def fresh():
+        c = KvCache(seqs, hk, d, 96, page_tokens=32, rope=rope)
+        c.append(start[0], start[1], 50)
+        return c
+
+    eager, want = fresh(), []
+    for kv, q in zip(steps, qs):
+        eager.append(kv[0], kv[1], 1)
+        want.append(torch.empty_like(q))
+        eager.attend(q, 0.2, want[-1])
+    assert eager.lens.tolist() == [59, 59]
+
+    cache = fresh()
+    lens = cache.lens  # what a caller holds stays the cache's lengths
+    kv, q, o = torch.empty_like(steps[0]), torch.empty_like(qs[0]), torch.empty_like(qs[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.append(kv[0], kv[1], 1)
+        cache.attend(q, 0.2, o)
+    assert cache.lens.tolist() == [50, 50]  # nothing ran yet
+    for i in range(9):
+        if i in (0, 4):  # an eager step, before the first replay too
+            got = torch.empty_like(qs[i])
+            cache.append(steps[i, 0], steps[i, 1], 1)
+            cache.attend(qs[i], 0.2, got)
+        else:
+            kv.copy_(steps[i])
+            q.copy_(qs[i])
+            graph.replay()
+            got = o
+        torch.cuda.synchronize()
+        assert lens.tolist() == cache.lens.tolist() == [51 + i, 51 + i]
+        assert cache.max_len >= 51 + i
+        # the captured call's work may be split elsewhere: two bf16 roundings and the sums' order
+        assert float((got.float() - want[i].float()).abs().max()) <= 2.0 ** -7 * float(want[i].float().abs().max())
+    for a, b in zip(cache.buffers, eager.buffers):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert L.losa_get_device_error() == 0

@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 import free_block_sparse_losa_b200 as L
 from free_block_sparse_losa_b200 import build as B
@@ -27,3 +28,45 @@ def test_append_strides_of_single_extents(lib):
     assert call(4, 1, (7, 96, 1, 96)) == UNSUPPORTED
     for hk, total, strides in ((1, 8, (95, 8, 96, 8)), (4, 1, (8, 96, 8, 95)), (4, 1, (8, -96, 8, 96))):
         assert call(hk, total, strides) == INVALID
+
+
+def test_lengths_of_captured_and_eager_appends(monkeypatch):
+    """KvCache's lengths without a GPU: a fake append that runs at once stands in for the call, a flag for the capture. A step
+    kept and run again goes on from the lengths the last append left, whichever kind it was."""
+    from free_block_sparse_losa_b200 import harness
+    capturing, kept = [False], []
+
+    def fake(cache, k, v, k8, v8, ks, vs, table, lens, new, indptr=None, new_lens=None, **kw):
+        def step():
+            new_lens.copy_(lens + new)
+        kept.append(step)
+        if not capturing[0]:
+            step()
+
+    monkeypatch.setattr(harness, "losa_cache_append", fake)
+    monkeypatch.setattr(harness.torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    cache = harness.KvCache(2, 1, 64, 96, page_tokens=32, device="cpu")
+    cache.append(None, None, 5)
+    before = cache.lens
+    cache.append(None, None, 2)
+    assert before.tolist() == [5, 5] and cache.lens.tolist() == [7, 7] and cache.max_len == 7
+    held = cache.lens
+    capturing[0] = True
+    real_copy, copies = torch.Tensor.copy_, []
+    monkeypatch.setattr(torch.Tensor, "copy_", lambda a, b: copies.append((a, b)))
+    cache.append(None, None, 1)
+    monkeypatch.setattr(torch.Tensor, "copy_", real_copy)
+    capturing[0] = False
+    graph = [kept[-1]] + [lambda a=a, b=b: a.copy_(b) for a, b in copies]
+    assert cache.lens.tolist() == [7, 7] and cache.max_len == 96
+    n = 7
+    for kind in "rrerer":
+        if kind == "e":
+            cache.append(None, None, 3)
+            n += 3
+        else:
+            for step in graph:
+                step()
+            n += 1
+        assert cache.lens.tolist() == held.tolist() == [n, n]
+    assert cache.max_len == 96
