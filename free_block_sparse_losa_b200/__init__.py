@@ -154,13 +154,14 @@ def _ptrs(*specs):
     device pointer (the caller vouches for its size). A tensor must have the expected dtype (if given), hold at least
     `numel` elements (if given), be contiguous and live on the current CUDA device, so that a wrong buffer is refused
     here instead of being read or written out of bounds on the GPU. The dtype, size and layout of every argument are
-    checked before any argument's device."""
-    torch = _torch()
+    checked before any argument's device. Raw pointers alone need no torch."""
     out, where = [], []
+    torch = None
     for t, name, dtype, numel in specs:
         if t is None or isinstance(t, int):
             out.append(t)
             continue
+        torch = torch or _torch()
         if dtype is not None and t.dtype is not _dtypes[dtype]:
             raise ValueError(f"{name}: expected torch.{dtype}, got {t.dtype}")
         if numel is not None and t.numel() < numel:

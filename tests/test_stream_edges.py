@@ -1,5 +1,8 @@
 """CPU checks of the streaming calls at the ends of what their documentation allows. No call here reaches the CUDA runtime."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -70,3 +73,22 @@ def test_lengths_of_captured_and_eager_appends(monkeypatch):
             n += 1
         assert cache.lens.tolist() == held.tolist() == [n, n]
     assert cache.max_len == 96
+
+
+def test_raw_pointers_need_no_torch(lib):
+    """Device pointers as ints and a stream handle: the calls that go through ctypes work where torch cannot be imported."""
+    code = """
+import sys
+sys.modules["torch"] = None
+import free_block_sparse_losa_b200 as L
+p = 0x10000
+s = L.make_shape(2, 300, 256, 128, 128, 128, "bf16")  # more tokens than rows: refused before anything is launched
+kw = dict(stream=0, raise_on_error=False)
+assert L.losa_sparse_attn(s, p, p, p, 0.1, p, p, p, 2 * p, **kw) == -1
+assert L.losa_dense_profile(s, p, p, p, 0.1, 2 * p, **kw) == -1
+assert L.losa_dense_profile_ws(s, p, p, p, 0.1, 2 * p, p, p, p, ws_bytes=16, **kw) == -1
+assert L.losa_select(s, p, 0.9, p, p, p, p, idx_capacity=8, ws_bytes=16, **kw) == -1
+assert L.losa_select_topk(s, p, 1, p, p, p, p, idx_capacity=8, ws_bytes=16, **kw) == -1
+assert L.losa_select_noalloc(s, p, 0.9, p, p, p, idx_capacity=8, **kw) == -1
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
