@@ -342,11 +342,12 @@ def losa_cache_attn_workspace_bytes(cache, heads, tokens, max_len=0) -> int:
 
 
 def losa_cache_attn(cache, q, k8, v8, k_scale, v_scale, page_table, lens, scale, o, lse=None, causal=True, max_len=0,
-                    workspace=None, stream=None, raise_on_error=True):
+                    workspace=None, stream=None, raise_on_error=True, ws_bytes=None):
     """q, o: (seqs, tokens, heads, head_dim) bf16, any strides but a contiguous last dimension; lse: (seqs, tokens,
-    heads). max_len bounds the lengths (0: the page table's capacity)."""
+    heads). max_len bounds the lengths (0: the page table's capacity). ws_bytes: the workspace's size, where it is a raw pointer
+    (0 otherwise: enough for a call that needs none) or less than the tensor."""
     st = (_binding or _fast()).cache_attn(cache, q, k8, v8, k_scale, v_scale, page_table, lens, scale, o, lse, causal,
-                                          max_len, workspace, stream)
+                                          max_len, workspace, ws_bytes, stream)
     return st if st == 0 else _check(st, "losa_cache_attn", raise_on_error)
 
 

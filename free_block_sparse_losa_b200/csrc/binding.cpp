@@ -284,9 +284,9 @@ PyObject* cache_append(PyObject*, PyObject* const* o, Py_ssize_t n) {
     });
 }
 
-// cache, q, k8, v8, k_scale, v_scale, page_table, lens, scale, o, lse, causal, max_len, workspace, stream
+// cache, q, k8, v8, k_scale, v_scale, page_table, lens, scale, o, lse, causal, max_len, workspace, ws_bytes, stream
 PyObject* cache_attn(PyObject*, PyObject* const* o, Py_ssize_t n) {
-    return guarded(n, 15, [&] {
+    return guarded(n, 16, [&] {
         Struct<losa_cache> cache(o[0], "cache");
         if (!cache.get()) throw Refused{"cache: expected the call's structure"};
         Args a;
@@ -299,17 +299,26 @@ PyObject* cache_attn(PyObject*, PyObject* const* o, Py_ssize_t n) {
         float* lse = (float*)a.buffer(o[10], "lse", at::kFloat, q.size(0) * q.size(1) * q.size(2));
         void* ws = a.buffer(o[13], "workspace", at::kFloat, -1, true);
         size_t ws_bytes = 0;
-        if (ws && THPVariable_Check(o[13])) {
-            const at::Tensor& w = THPVariable_Unpack(o[13]);
-            ws_bytes = (size_t)w.numel() * w.element_size();
+        const bool says = o[14] != Py_None;
+        if (says) {
+            const int64_t b = whole(o[14]);
+            if (b < 0) throw Refused{"ws_bytes: out of range"};
+            ws_bytes = (size_t)b;
         }
+        if (o[13] != Py_None && THPVariable_Check(o[13])) {
+            const at::Tensor& w = THPVariable_Unpack(o[13]);
+            const size_t have = (size_t)w.numel() * w.element_size();
+            if (says && have < ws_bytes)
+                throw Refused{"workspace: holds " + std::to_string(have) + " bytes, ws_bytes says " + std::to_string(ws_bytes)};
+            if (!says) ws_bytes = have;
+        }  // a raw pointer without its size counts as empty, which is enough for calls that need no workspace
         a.check_devices();
         const int32_t heads = extent(q.size(2), "q"), tokens = extent(q.size(1), "q"), causal = truth(o[11]);
         const int64_t qs[3] = {q.stride(0), q.stride(1), q.stride(2)};
         const int64_t os[3] = {out.stride(0), out.stride(1), out.stride(2)};
         const float scale = real(o[8]);
         const int32_t max_len = int32_of(o[12], "max_len");
-        cudaStream_t stream = stream_of(o[14]);
+        cudaStream_t stream = stream_of(o[15]);
         return unlocked([&] {
             return g_cache_attn(cache.get(), heads, tokens, causal, pq, qs[0], qs[1], qs[2], p.table, p.lens, p.k8, p.v8,
                                 p.k_scale, p.v_scale, scale, max_len, po, os[0], os[1], os[2], lse, ws, ws_bytes, stream);

@@ -323,3 +323,27 @@ def test_a_captured_harness_step_advances_with_every_replay():
     for a, b in zip(cache.buffers, eager.buffers):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     assert L.losa_get_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_decode_with_a_raw_workspace():
+    """The workspace as a device pointer and its size gives what the tensor gives; too small a size is refused."""
+    require_gpu()
+    g = gen(76)
+    lens, hk, page, d, heads = [5000, 77], 1, 64, 64, 2
+    *pool, table = poisoned_cache(g, lens, hk, page, d, -(-max(lens) // page))
+    q = torch.randn(2, 1, heads, d, generator=g, device="cuda").bfloat16()
+    want = decode_call(q, pool, table, lens, 0.1)
+    cache = L.make_cache(hk, d, page, pool[0].shape[0], 2, table.shape[1])
+    need = L.losa_cache_attn_workspace_bytes(cache, heads, 1)
+    ws = torch.empty(need + 64, dtype=torch.uint8, device="cuda")
+    for space in (ws.data_ptr(), ws):
+        o, lse = torch.full_like(q, 9.0), torch.full((2, 1, heads), 9.0, device="cuda")
+        assert L.losa_cache_attn(cache, q, *pool, table, ints(lens), 0.1, o, lse=lse, workspace=space, ws_bytes=need) == 0
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        assert L.losa_cache_attn(cache, q, *pool, table, ints(lens), 0.1, o, workspace=space, ws_bytes=need - 1,
+                                 raise_on_error=False) == -3
+    bare = lambda max_len: L.losa_cache_attn(cache, q, *pool, table, ints([900, 77]), 0.1, o, max_len=max_len,  # noqa: E731
+                                             workspace=ws.data_ptr(), raise_on_error=False)
+    assert bare(900) == 0 and bare(0) == -3  # without a size it counts as empty
+    assert L.losa_get_device_error() == 0

@@ -92,3 +92,21 @@ assert L.losa_select_topk(s, p, 1, p, p, p, p, idx_capacity=8, ws_bytes=16, **kw
 assert L.losa_select_noalloc(s, p, 0.9, p, p, p, idx_capacity=8, **kw) == -1
 """
     subprocess.run([sys.executable, "-c", code], check=True, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+
+def test_workspace_bytes(lib):
+    """A raw workspace comes with its size, as for the other calls; a tensor's size is its own unless less is said."""
+    c = L.make_cache(2, 128, 32, 6, 2, 3)
+    t = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt)  # noqa: E731
+    q, o = t(2, 1, 4, 128), t(2, 1, 4, 128)
+
+    def call(**kw):
+        return L.losa_cache_attn(c, q, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0.1, o, stream=0, raise_on_error=False, **kw)
+
+    with pytest.raises(ValueError, match="workspace: holds 64 bytes, ws_bytes says 65"):
+        call(workspace=t(64, dt=torch.uint8), ws_bytes=65)
+    with pytest.raises(ValueError, match="ws_bytes: out of range"):
+        call(workspace=FAKE, ws_bytes=-1)
+    for kw in (dict(workspace=FAKE), dict(workspace=FAKE, ws_bytes=64), dict(workspace=t(64, dt=torch.uint8), ws_bytes=64), dict(ws_bytes=0), {}):
+        with pytest.raises(ValueError, match="q: expected a CUDA tensor"):  # the last check: these got past the sizes
+            call(**kw)
