@@ -94,10 +94,12 @@ class LayerBuffers:
 
     def pack_qkv(self, qkv, rope, out=None, positions=None, start=None, stream=None):
         """A fused projection's output (batch, N, 3, heads / batch, d), any strides but a contiguous last dimension, as the
-        calls' q, k, v: query and key rotated, head-major, padding rows zero. Returns views of one (3, H, Np, d) buffer."""
+        calls' q, k, v: query and key rotated, head-major, padding rows zero. Returns views of one (3, H, Np, d) buffer,
+        which belongs to the call's stream if it is made here."""
         batch, n, _, heads, d = qkv.shape
         if out is None:
-            out = torch.empty((3, self.heads, self.n_padded, self.head_dim), dtype=qkv.dtype, device=qkv.device)
+            with _on_stream(stream):
+                out = torch.empty((3, self.heads, self.n_padded, self.head_dim), dtype=qkv.dtype, device=qkv.device)
         y = out.view(3, batch, heads, self.n_padded, d).permute(0, 1, 3, 2, 4)
         losa_rope_apply(rope, qkv.permute(2, 0, 1, 3, 4), y, rotate=0b011, positions=positions, start=start, stream=stream)
         return out[0], out[1], out[2]

@@ -347,3 +347,28 @@ def test_decode_with_a_raw_workspace():
                                              workspace=ws.data_ptr(), raise_on_error=False)
     assert bare(900) == 0 and bare(0) == -3  # without a size it counts as empty
     assert L.losa_get_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_packing_on_a_side_stream():
+    """pack_qkv on another stream while the current one still writes memory that it has given back to the allocator."""
+    require_gpu()
+    from free_block_sparse_losa_b200.harness import LayerBuffers
+    g = gen(77)
+    heads, n, d = 8, 1000, 128
+    rope = L.make_rope(d, (44, 42, 42), (25, 20))
+    layer = LayerBuffers(heads, n, 1024, d, 128, "bf16")
+    qkv = torch.randn(1, n, 3, heads, d, generator=g, device="cuda").bfloat16()
+    want = [t.clone() for t in layer.pack_qkv(qkv, rope)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        late = torch.empty(3, heads, 1024, d, dtype=torch.bfloat16, device="cuda")
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        late.fill_(5.0)
+        del late  # its memory is free for the current stream's next tensor of this size, behind the fill
+        got = layer.pack_qkv(qkv, rope, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del got
+    assert L.losa_get_device_error() == 0

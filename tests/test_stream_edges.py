@@ -110,3 +110,30 @@ def test_workspace_bytes(lib):
     for kw in (dict(workspace=FAKE), dict(workspace=FAKE, ws_bytes=64), dict(workspace=t(64, dt=torch.uint8), ws_bytes=64), dict(ws_bytes=0), {}):
         with pytest.raises(ValueError, match="q: expected a CUDA tensor"):  # the last check: these got past the sizes
             call(**kw)
+
+
+def test_packed_projection_is_allocated_on_the_calls_stream(lib, monkeypatch):
+    """pack_qkv's own buffer belongs to the stream that fills it: memory that the current stream still uses must not be
+    handed to a call on another one."""
+    from free_block_sparse_losa_b200 import harness
+    inside, seen = [], []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            inside.append(self.stream)
+
+        def __exit__(self, *a):
+            inside.pop()
+
+    real = torch.empty
+    layer = harness.LayerBuffers(4, 100, 128, 64, 128, "f32", device="cpu")
+    monkeypatch.setattr(harness, "_on_stream", On)
+    monkeypatch.setattr(harness, "losa_rope_apply", lambda *a, **kw: seen.append(("call", kw["stream"])))
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: seen.append(("alloc", list(inside))) or real(*a, **kw))
+    for stream in (None, 77, "side"):
+        layer.pack_qkv(torch.zeros(2, 100, 3, 2, 64), None, stream=stream)
+        assert seen == [("alloc", [stream]), ("call", stream)]
+        seen.clear()
