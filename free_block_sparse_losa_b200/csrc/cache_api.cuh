@@ -16,8 +16,10 @@ bool rope_ok(const losa_rope* r, int head_dim) {
     return std::isfinite(r->theta) && r->theta > 0.0;
 }
 
-// Turns per unit of position of every pair, as fractions of 2^64. One power per axis, then products, in 64-bit mantissas:
-// a pair's step is off by a few units of 2^-64.
+// Turns per unit of position of every pair, as fractions of 2^64. One power per axis, then i products for pair i, in 64-bit
+// mantissas: f is off by i (2^-63 + 2^-64) of itself at most (the power's last place and a rounding each), which for 127
+// products of at most 1 / (2 pi min(theta, 1)) is below 2^-58 / min(theta, 1); for theta = 10000 and 64 pairs, whose f shrinks
+// meanwhile, below 3 units of 2^-64.
 RopeArgs rope_args(const losa_rope* r) {
     RopeArgs a;
     a.gy = r->grid_y;

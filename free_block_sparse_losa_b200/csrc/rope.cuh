@@ -4,8 +4,9 @@
 //
 // A token at (t, y, x) turns pair i of an axis of m dimensions by pos * theta^(-2i/m). Angles are kept in turns as 64-bit
 // fixed-point fractions: the host rounds theta^(-2i/m) / 2 pi to a multiple of 2^-64, and pos * step wraps modulo one
-// turn by itself, so the reduction of a far position's angle is one exact integer product (the error is pos * 2^-65
-// turns). The nearest quarter turn is split off, and the rest, at most an eighth of a turn, goes through sincospif.
+// turn by itself, so the reduction of a far position's angle is one exact integer product (the error is pos times
+// the step's, see rope_args). The nearest quarter turn is split off, and the rest, at most an eighth of a turn, goes through
+// sincospif.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>

@@ -197,7 +197,8 @@ enum { LOSA_ROPE_INTERLEAVED = 0, LOSA_ROPE_HALVES = 1 };
  * the next axis_dims[2] with x; what is left is not rotated. Within an axis of m dimensions pair i (0 <= i < m / 2) turns
  * by pos * theta^(-2 i / m); it is made of dimensions (2i, 2i + 1) of the axis's section (interleaved) or (i, i + m / 2)
  * (halves). Token n of the grid sits at t = n / (grid_y grid_x), y = (n / grid_x) mod grid_y, x = n mod grid_x, plus the
- * offsets. Angles are exact to 2^-32 of a turn at any 32-bit position. */
+ * offsets; positions stay within 32 bits. An angle is off by at most |pos| 2^-58 / min(theta, 1) + 2^-33 turns: 2^-26.9 at
+ * any 32-bit position for theta >= 1 (2^-31 for theta = 10000). */
 typedef struct {
     int32_t head_dim;      /* d, at most 256; a row is a multiple of 16 bytes */
     int32_t axis_dims[3];  /* even, their sum at most d                      */

@@ -372,3 +372,37 @@ def test_packing_on_a_side_stream():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         del got
     assert L.losa_get_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("theta", [1e-4, 0.3, 1.0, 1.0001, 37.5, 10000.0, 1e6, 1e30])
+@pytest.mark.parametrize("halves", [False, True])
+def test_rope_angles_at_far_positions(theta, halves):
+    """Any theta, at positions over all of 32 bits, against angles in 60 decimal digits. The documented bound of an angle,
+    |pos| 2^-58 / min(theta, 1) + 2^-33 turns, on top of what cosine, sine and the products are rounded by."""
+    require_gpu()
+    from decimal import Decimal, localcontext
+    g = gen(73)
+    d, dims = 64, (20, 22, 20)
+    pos = [[2 ** 31 - 1, -2 ** 31, 1999999999], [1, -1, 0], [123456, -98765, 1 << 20], [-7, 1 << 30, 33]]
+    x = torch.randn(1, 1, len(pos), 2, d, generator=g, device="cuda")
+    y = torch.empty_like(x)
+    L.losa_rope_apply(L.make_rope(d, dims, (4, 4), theta=theta, halves=halves), x, y, positions=ints([pos]))
+    assert L.losa_get_device_error() == 0
+    pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+    xs, ys = x[0, 0].double().cpu(), y[0, 0].double().cpu()
+    for i, triple in enumerate(pos):
+        at = 0
+        for p, m in zip(triple, dims):
+            for j in range(m // 2):
+                with localcontext() as ctx:
+                    ctx.prec = 60
+                    turns = Decimal(p) * (Decimal(theta) ** (Decimal(-2 * j) / m)) / (2 * pi)
+                    angle = float((turns % 1) * 2 * pi)
+                a, b = (at + j, at + m // 2 + j) if halves else (at + 2 * j, at + 2 * j + 1)
+                c, s = math.cos(angle), math.sin(angle)
+                off = 2 * math.pi * (abs(p) * 2.0 ** -58 / min(theta, 1.0) + 2.0 ** -33) + 6 * 2.0 ** -24
+                size = xs[i, :, a].abs() + xs[i, :, b].abs()
+                assert bool(((ys[i, :, a] - (xs[i, :, a] * c - xs[i, :, b] * s)).abs() <= off * size + 1e-38).all()), (p, j)
+                assert bool(((ys[i, :, b] - (xs[i, :, a] * s + xs[i, :, b] * c)).abs() <= off * size + 1e-38).all()), (p, j)
+            at += m
