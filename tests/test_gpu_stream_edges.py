@@ -7,7 +7,8 @@ import torch
 
 import free_block_sparse_losa_b200 as L
 from tests.gpu_util import require_gpu
-from tests.test_gpu_stream import attend, attn_close, check_blocks, dense, gen, make_pool, poisoned_cache
+from tests.test_gpu_stream import (append_reference, attend, attn_close, check_blocks, dense, gen, grid_positions, make_pool,
+                                   poisoned_cache, random_lists, turn)
 
 
 def ints(v):
@@ -406,3 +407,98 @@ def test_rope_angles_at_far_positions(theta, halves):
                 assert bool(((ys[i, :, a] - (xs[i, :, a] * c - xs[i, :, b] * s)).abs() <= off * size + 1e-38).all()), (p, j)
                 assert bool(((ys[i, :, b] - (xs[i, :, a] * s + xs[i, :, b] * c)).abs() <= off * size + 1e-38).all()), (p, j)
             at += m
+
+
+def codes_near(got, want, off):
+    """Codes equal the reference rounded to e4m3, or that of a value at most `off` away."""
+    near = [(want + s * off).clamp(-448, 448).float().to(torch.float8_e4m3fn).double() for s in (0, 1, -1)]
+    ok = (got.double() == near[0]) | (got.double() == near[1]) | (got.double() == near[2])
+    assert bool(ok.all()), int((~ok).sum())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,page,hk,halves", [(128, 128, 3, True), (64, 32, 5, False), (128, 64, 2, False)])
+def test_append_of_many_fp32_pages(d, page, hk, halves):
+    """Thousands of fp32 tokens in ragged sequences, against the 64-bit form. A rotated value is a c - b s in fp32: off by at
+    most 6 * 2^-24 (|a| + |b|), which among millions of them is more than 1e-5 of a value that cancels to a few per cent, so
+    the band around a rounding border is this bound (over the block's scale) and not a share of the value; a value that is not
+    rotated is exact."""
+    require_gpu()
+    g = gen(72)
+    held, new = [0, 77, page - 1, 500], [5000, 1, 3001, 0]
+    seqs, width = 4, -(-5100 // page)
+    pool = make_pool(g, seqs * width, hk, page, d)
+    before = [t.clone() for t in pool]
+    table = torch.randperm(seqs * width, generator=g, device="cuda").view(seqs, width).int()
+    kv = torch.randn(sum(new), 2, hk, d, generator=g, device="cuda")
+    ptr = [sum(new[:i]) for i in range(seqs + 1)]
+    dims = (20, 22, 20) if d == 64 else (44, 42, 42)
+    out = ints([0] * seqs)
+    L.losa_cache_append(L.make_cache(hk, d, page, seqs * width, seqs, width), kv[:, 0], kv[:, 1], *pool, table, ints(held), 5000,
+                        indptr=ints(ptr), new_lens=out, rope=L.make_rope(d, dims, (30, 52), halves=halves))
+    assert L.losa_get_device_error() == 0
+    assert out.tolist() == [h + m for h, m in zip(held, new)]
+    per = [kv[ptr[b]:ptr[b + 1]].double() for b in range(seqs)]
+    keys = [turn(x[:, 0], grid_positions(torch.arange(held[b], held[b] + new[b]), 30, 52)[:, None], dims, halves)
+            for b, x in enumerate(per)]
+    size = []  # |a| + |b| of every element of k
+    for x in per:
+        z, at = x[:, 0].abs().clone(), 0
+        for m in dims:
+            i = torch.arange(m // 2, device="cuda")
+            a, b = (at + i, at + m // 2 + i) if halves else (at + 2 * i, at + 2 * i + 1)
+            z[..., a] = z[..., b] = x[:, 0, :, a].abs() + x[:, 0, :, b].abs()
+            at += m
+        z[..., at:] = 0
+        size.append(z)
+    for x, codes, scale, was8, was, of in ((keys, pool[0], pool[2], before[0], before[2], size),
+                                           ([x[:, 1] for x in per], pool[1], pool[3], before[1], before[3], None)):
+        want, ws = append_reference(x, was8, was, table, held, new, page)
+        assert torch.equal(scale.double(), ws)
+        off = torch.zeros_like(want)
+        for b in range(seqs if of else 0):
+            for blk in range(held[b] // page, -(-(held[b] + new[b]) // page)):
+                lo, hi = max(held[b] - blk * page, 0), min(page, held[b] + new[b] - blk * page)
+                pg = int(table[b, blk])
+                if hi > lo:
+                    rows = of[b][blk * page + lo - held[b]:blk * page + hi - held[b]]
+                    off[pg, :, lo:hi] = (6 * 2.0 ** -24 * rows / ws[pg][None, :, None]).transpose(0, 1)
+        codes_near(codes, want, off)
+
+
+@pytest.mark.gpu
+def test_blocks_of_more_items_than_one_window():
+    """More than 32 rounds of items a CTA (the reader's window): short lists, some empty, in a shuffled order."""
+    require_gpu()
+    g = gen(70)
+    page, heads, n = 32, 24, 300 * 128 - 5
+    items = heads * 300
+    assert items > 33 * torch.cuda.get_device_properties(0).multi_processor_count
+    lens = [1000]
+    width = -(-lens[0] // page) + 1
+    *pool, table = poisoned_cache(g, lens, 3, page, 128, width)
+    q = torch.randn(heads, 300 * 128, 128, generator=g, device="cuda").bfloat16()
+    indptr, blocks = random_lists(g, items, width, 1, 2, empty_every=11)
+    order = torch.randperm(items, generator=g, device="cuda").int()
+    o, lse = blocks_call(q, pool, table, lens, page, heads, 3, n, 0.03, indptr=indptr, kv_block_idx=blocks, order=order)
+    assert L.losa_get_device_error() == 0
+    check_blocks(q, o, lse, pool, table, lens, page, heads, 3, n, 0.03, indptr, blocks, items=sorted(order[::29].tolist()))
+    again = blocks_call(q, pool, table, lens, page, heads, 3, n, 0.03, indptr=indptr, kv_block_idx=blocks)
+    assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,hk,heads,tokens,seqs,top", [(128, 2, 4, 1, 70, 3000), (64, 1, 8, 4, 37, 5000), (128, 1, 40, 1, 33, 2000),
+                                                        (128, 1, 24, 1, 3, 9000)])
+def test_decode_of_many_ragged_sequences(d, hk, heads, tokens, seqs, top):
+    """More sequences than a warp has lanes, and 17 to 40 rows to a kv head, in ranges that cross the sequences' borders."""
+    require_gpu()
+    g = gen(71)
+    page = 64
+    lens = [0 if b % 5 == 2 else max(1, (top * (b * 7919 % 101)) // 100) for b in range(seqs)]
+    lens[-1] = top
+    *pool, table = poisoned_cache(g, lens, hk, page, d, -(-top // page))
+    q = torch.randn(seqs, tokens, heads, d, generator=g, device="cuda").bfloat16()
+    o, lse = decode_call(q, pool, table, lens, 0.05)
+    assert L.losa_get_device_error() == 0
+    check_decode(q, o, lse, pool, table, lens, 0.05)
