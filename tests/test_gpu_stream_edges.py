@@ -502,3 +502,29 @@ def test_decode_of_many_ragged_sequences(d, hk, heads, tokens, seqs, top):
     o, lse = decode_call(q, pool, table, lens, 0.05)
     assert L.losa_get_device_error() == 0
     check_decode(q, o, lse, pool, table, lens, 0.05)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens,max_len", [(1, 64), (3, 0)])
+def test_scales_at_the_ends_of_their_range(tokens, max_len):
+    """Value blocks at 2^-40, 1 and 2^60 next to each other: the quiet ones count in the denominator as the loud ones do. Key
+    blocks at 2^-40 and 2^-6."""
+    require_gpu()
+    g = gen(78)
+    lens, hk, page, heads, n = [1500, 200], 2, 64, 4, 256
+    k8, v8, ks, vs, table = poisoned_cache(g, lens, hk, page, 128, -(-max(lens) // page))
+    pick = lambda of: of[torch.randint(len(of), ks.shape, generator=g, device="cuda")]  # noqa: E731
+    for b, count in enumerate(lens):
+        used = table[b, :-(-count // page)].long()
+        ks[used] = pick(torch.tensor([2.0 ** -40, 2.0 ** -6], device="cuda"))[used]
+        vs[used] = pick(torch.tensor([2.0 ** -40, 1.0, 2.0 ** 60], device="cuda"))[used]
+    pool = (k8, v8, ks, vs)
+    q = torch.randn(2, tokens, heads, 128, generator=g, device="cuda").bfloat16()
+    o, lse = decode_call(q, pool, table, lens, 0.1, max_len=max_len)
+    check_decode(q, o, lse, pool, table, lens, 0.1)
+    qb = torch.randn(2 * heads, n, 128, generator=g, device="cuda").bfloat16()
+    indptr, blocks = random_lists(g, 2 * heads * 2, table.shape[1], 1, 9)
+    for kw in ({}, dict(indptr=indptr, kv_block_idx=blocks)):
+        o, lse = blocks_call(qb, pool, table, lens, page, heads, hk, n, 0.1, **kw)
+        assert L.losa_get_device_error() == 0
+        check_blocks(qb, o, lse, pool, table, lens, page, heads, hk, n, 0.1, kw.get("indptr"), kw.get("kv_block_idx"))
