@@ -152,8 +152,9 @@ __device__ __forceinline__ int key_of_column(int n) { return (n & 1) ? ((n - 1) 
 template <int D> constexpr uint32_t kCaTile = kCaKeys * D;  // bytes of a warp's key or value tile
 // NB: 8-row groups of a CTA's row tile. Up to eight rows, half the accumulators and products are enough.
 template <int NB> constexpr int kCaRows = 8 * NB;
-// Tiles in flight per warp and CTAs per SM: 128 KB on their way to an SM. More (three tiles, or three CTAs, which eight
-// rows have room for) queue in the memory system and let some SMs finish well before others: 84..86 against 80 us on eight
+// Tiles in flight per warp and CTAs per SM: 128 KB on their way to an SM with 128 dimensions (64 KB
+// with 64). More (three tiles, or three CTAs, which
+// eight rows have room for) queue in the memory system and let some SMs finish well before others: 84..86 against 80 us on eight
 // ragged streams of four rows, 95 against 92 us on two long ones of twelve.
 constexpr int kCaStages = 2;
 constexpr int kCaCtas = 2;
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(NW * 32, kCaCtas * kCaWarps / NW)
     const int tile = unit % a.tiles, kvh = unit / a.tiles;
     const int64_t unit_pos = seq_pos + (int64_t)unit * n_tiles;
     const int t0 = (int)(pos - unit_pos), t1 = n_tiles == 0 ? 0 : (int)min((int64_t)n_tiles, stop - unit_pos);
-    const int mine = max(0, (t1 - t0 - warp + NW - 1) / NW);  // this warp's tiles: t0 + warp, + 4, ...
+    const int mine = max(0, (t1 - t0 - warp + NW - 1) / NW);  // this warp's tiles: t0 + warp, + NW, ...
 
     // Raw query rows, row 8 nb + g of the tile: asked for before the copies of codes, which would hold them up.
     const int n_rows = a.tokens * a.group;

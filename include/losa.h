@@ -236,7 +236,7 @@ losa_status losa_rope_apply(const losa_rope* rope, int32_t dtype, const losa_tok
  * [n_pages][kv_heads] fp32; a code stands for code * scale. Sequence b's block j (tokens j page_tokens ...) is page
  * page_table[b][j] (int32 [seqs][table_stride]) of the pool; its length is lens[b] (int32 [seqs]). head_dim is 64 or 128,
  * page_tokens 32, 64 or 128 (else LOSA_ERR_UNSUPPORTED); n_pages * kv_heads * page_tokens must stay below 2^31. Scales are
- * positive; losa_cache_append writes powers of two between 2^-40 and 2^60. */
+ * numbers between 2^-40 and 2^60; losa_cache_append writes powers of two. */
 typedef struct {
     int32_t kv_heads, head_dim, page_tokens, n_pages;
     int32_t seqs, table_stride;
@@ -256,7 +256,7 @@ typedef struct {
  * or the scale a part-full block already has if that is larger; where the scale grows, the block's held codes are rounded
  * to it again. New values are rounded to nearest, infinities and values out of range saturate, NaN stays NaN. Nothing
  * else of the pool is written: codes behind a sequence's last token keep what they hold.
- * The pages a call writes must belong to one sequence each. A token count, length, row or page out of range sets the
+ * The pages a call writes must belong to one block of one sequence each. A token count, length, row or page out of range sets the
  * device error word (LOSA_ERR_DEVICE_FAULT); the tokens concerned are not stored.
  */
 losa_status losa_cache_append(const losa_cache* cache, const losa_rope* rope, int32_t dtype, const void* k,
