@@ -152,10 +152,9 @@ __device__ __forceinline__ int key_of_column(int n) { return (n & 1) ? ((n - 1) 
 template <int D> constexpr uint32_t kCaTile = kCaKeys * D;  // bytes of a warp's key or value tile
 // NB: 8-row groups of a CTA's row tile. Up to eight rows, half the accumulators and products are enough.
 template <int NB> constexpr int kCaRows = 8 * NB;
-// Tiles in flight per warp and CTAs per SM: 128 KB on their way to an SM with 128 dimensions (64 KB
-// with 64). More (three tiles, or three CTAs, which
-// eight rows have room for) queue in the memory system and let some SMs finish well before others: 84..86 against 80 us on eight
-// ragged streams of four rows, 95 against 92 us on two long ones of twelve.
+// Tiles in flight per warp and CTAs per SM: 128 KB on their way to an SM with 128 dimensions, 64 KB with 64. At 128 dimensions
+// more (three tiles, or three CTAs, which eight rows have room for) queue in the memory system and let some SMs finish well
+// before others: 84..86 against 80 us on eight ragged streams of four rows, 95 against 92 us on two long ones of twelve.
 constexpr int kCaStages = 2;
 constexpr int kCaCtas = 2;
 template <int D, int NB, int NW> constexpr uint32_t kCaSmem =

@@ -256,8 +256,8 @@ typedef struct {
  * or the scale a part-full block already has if that is larger; where the scale grows, the block's held codes are rounded
  * to it again. New values are rounded to nearest, infinities and values out of range saturate, NaN stays NaN. Nothing
  * else of the pool is written: codes behind a sequence's last token keep what they hold.
- * The pages a call writes must belong to one block of one sequence each. A token count, length, row or page out of range sets the
- * device error word (LOSA_ERR_DEVICE_FAULT); the tokens concerned are not stored.
+ * The pages a call writes must belong to one block of one sequence each. A token count, length, row or page out of range
+ * sets the device error word (LOSA_ERR_DEVICE_FAULT); the tokens concerned are not stored.
  */
 losa_status losa_cache_append(const losa_cache* cache, const losa_rope* rope, int32_t dtype, const void* k,
                               int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
@@ -280,10 +280,9 @@ losa_status losa_cache_append(const losa_cache* cache, const losa_rope* rope, in
  *   workspace : scratch of losa_cache_attn_workspace_bytes(cache, heads, tokens, max_len) bytes, 16-byte aligned (may be
  *               NULL where that is 0), used during the call only; calls that can overlap need their own.
  * A row that sees no key (an empty sequence) gets o = 0 and lse = -inf. A row with an infinity or NaN in q gets NaN in o and
- * lse where it sees a key, whatever the signs of the codes. Logits, weights' sums and O are fp32; weights
- * are rounded to fp16 for the product with V. Codes of slots that hold no token are never used, whatever they are. A length
- * outside [0, capacity] or a page out of range sets the device error word (LOSA_ERR_DEVICE_FAULT); the keys concerned
- * are left out.
+ * lse where it sees a key, whatever the signs of the codes. Logits, weights' sums and O are fp32; weights are rounded to
+ * fp16 for the product with V. Codes of slots that hold no token are never used, whatever they are. A length outside
+ * [0, capacity] or a page out of range sets the device error word (LOSA_ERR_DEVICE_FAULT); the keys concerned are left out.
  */
 losa_status losa_cache_attn(const losa_cache* cache, int32_t heads, int32_t tokens, int32_t causal, const void* q,
                             int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
@@ -304,10 +303,10 @@ losa_status losa_cache_attn(const losa_cache* cache, int32_t heads, int32_t toke
  *   order     : work order, or NULL, as for losa_sparse_attn.
  *   scale     : logit scale, > 0.
  * A row that sees no key (an empty list, an empty sequence) gets o = 0 and lse = -inf; one with an infinity or NaN in q gets
- * NaN in both where it sees a key. Query elements below 2^-9 of their
- * row's largest are off by at most 2^-17 of it; weights are rounded to fp16 for the product with V; the rest is fp32. Codes of
- * slots that hold no token are never used. A block, page, length, offset or work-order entry out of range sets the device
- * error word (LOSA_ERR_DEVICE_FAULT); the blocks concerned are left out.
+ * NaN in both where it sees a key. Query elements below 2^-9 of their row's largest are off by at most 2^-17 of it; weights
+ * are rounded to fp16 for the product with V; the rest is fp32. Codes of slots that hold no token are never used. A block,
+ * page, length, offset or work-order entry out of range sets the device error word (LOSA_ERR_DEVICE_FAULT); the blocks
+ * concerned are left out.
  */
 losa_status losa_cache_sparse_attn(const losa_shape* shape, const losa_cache* cache, const void* q,
                                    const int32_t* page_table, const int32_t* lens, const void* k8, const void* v8,
