@@ -35,6 +35,10 @@ def _on_stream(stream):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
+def _capturing(t):
+    return t.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
 @dataclass
 class LayerBuffers:
     heads: int
@@ -120,9 +124,9 @@ class LayerBuffers:
 class KvCache:
     """A layer's paged 8-bit cache for `seqs` sequences of up to `capacity` tokens: its pool, page table (each sequence's
     pages in order) and lengths, which live on the device. An eager append leaves the lengths before it where they were and
-    flips to another buffer; from the first append captured into a graph on, `lens` is one tensor that every append advances,
-    eager or replayed, so that both go on from each other. max_len bounds the lengths on the host; as replays are not seen
-    there, it is the capacity from the first captured append on."""
+    flips to another buffer; once a call or a reading of `lens` is captured into a graph, `lens` stays one tensor that every
+    append advances, eager or replayed, so that both go on from each other. max_len bounds the lengths on the host; as replays
+    are not seen there, it is the capacity from the first captured append on."""
 
     def __init__(self, seqs, kv_heads, head_dim, capacity, page_tokens=128, rope=None, device="cuda"):
         self.seqs, self.page_tokens, self.rope = seqs, page_tokens, rope
@@ -136,11 +140,12 @@ class KvCache:
         self.page_table = torch.arange(seqs * width, dtype=torch.int32, device=device).view(seqs, width)
         self._lens = torch.zeros((2, seqs), dtype=torch.int32, device=device)
         self._now = 0
-        self._captured = False
+        self._fixed = self._replayed = False  # a graph holds the lengths' address; a graph may append
         self.max_len = 0
 
     @property
     def lens(self):
+        self._fixed |= _capturing(self._lens)
         return self._lens[self._now]
 
     @property
@@ -150,30 +155,32 @@ class KvCache:
     def append(self, k, v, new_tokens, indptr=None, positions=None, stream=None):
         """k, v: (tokens, kv_heads, d) of all sequences; new_tokens of each, or at most that many with indptr."""
         nxt = 1 - self._now
-        losa_cache_append(self.cache, k, v, *self.buffers, self.lens, new_tokens, indptr=indptr, new_lens=self._lens[nxt],
-                          rope=self.rope, positions=positions, stream=stream)
-        capacity = self.cache.table_stride * self.page_tokens
         with _on_stream(stream):
-            self._captured |= torch.cuda.is_current_stream_capturing()
-            if self._captured:
-                self.lens.copy_(self._lens[nxt])
-        if not self._captured:
-            self._now = nxt
-        self.max_len = capacity if self._captured else min(self.max_len + int(new_tokens), capacity)
+            lens = self.lens
+            losa_cache_append(self.cache, k, v, *self.buffers, lens, new_tokens, indptr=indptr, new_lens=self._lens[nxt],
+                              rope=self.rope, positions=positions, stream=stream)
+            self._replayed |= _capturing(self._lens)
+            if self._fixed:
+                lens.copy_(self._lens[nxt])
+            else:
+                self._now = nxt
+        capacity = self.cache.table_stride * self.page_tokens
+        self.max_len = capacity if self._replayed else min(self.max_len + int(new_tokens), capacity)
 
     def attend(self, q, scale, o, lse=None, causal=True, stream=None):
         """The last tokens q (seqs, tokens, heads, d), appended before, over the whole cache. The workspace comes from the
         allocator on the call's stream every time: calls on several streams, and captured ones, each have their own."""
         need = losa_cache_attn_workspace_bytes(self.cache, q.shape[2], q.shape[1], self.max_len)
-        workspace = None
-        if need:
-            with _on_stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=self.k8.device)
-        losa_cache_attn(self.cache, q, *self.buffers, self.lens, scale, o, lse=lse, causal=causal, max_len=self.max_len,
+        with _on_stream(stream):
+            lens = self.lens
+            workspace = torch.empty(need, dtype=torch.uint8, device=self.k8.device) if need else None
+        losa_cache_attn(self.cache, q, *self.buffers, lens, scale, o, lse=lse, causal=causal, max_len=self.max_len,
                         workspace=workspace, stream=stream)
 
     def sparse(self, layer, q, scale, out, lse=None, lists=True, order=True, stream=None):
         """Query blocks of a layer (LayerBuffers with block_k = page_tokens) over its frozen lists, or over every block."""
-        losa_cache_sparse_attn(layer.shape, self.cache, q, *self.buffers, self.lens, scale, out,
+        with _on_stream(stream):
+            lens = self.lens
+        losa_cache_sparse_attn(layer.shape, self.cache, q, *self.buffers, lens, scale, out,
                                indptr=layer.indptr if lists else None, kv_block_idx=layer.kv_idx if lists else None,
                                order=layer.order if lists and order else None, lse=lse, stream=stream)

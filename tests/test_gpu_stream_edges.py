@@ -528,3 +528,39 @@ def test_scales_at_the_ends_of_their_range(tokens, max_len):
         o, lse = blocks_call(qb, pool, table, lens, page, heads, hk, n, 0.1, **kw)
         assert L.losa_get_device_error() == 0
         check_blocks(qb, o, lse, pool, table, lens, page, heads, hk, n, 0.1, kw.get("indptr"), kw.get("kv_block_idx"))
+
+
+@pytest.mark.gpu
+def test_captured_reads_follow_eager_appends():
+    """A captured rotation that starts at the cache's lengths, a captured decode and a captured blocked call, replayed behind
+    eager appends, give what eager calls give."""
+    require_gpu()
+    from free_block_sparse_losa_b200.harness import KvCache, LayerBuffers
+    g = gen(79)
+    hk, d, page = 2, 128, 32
+    rope = L.make_rope(d, (44, 42, 42), (3, 5))
+    cache = KvCache(1, hk, d, 400, page_tokens=page, rope=rope)
+    layer = LayerBuffers(hk, 100, 128, d, 128, "bf16", block_k=page)
+    kv = torch.randn(8, 2, 50, hk, d, generator=g, device="cuda").bfloat16()
+    x, qb = torch.randn(1, 2, hk, d, generator=g, device="cuda").bfloat16(), torch.randn(hk, 128, d, generator=g, device="cuda").bfloat16()
+
+    def step(r, o, ob, stream=None):
+        L.losa_rope_apply(rope, x[None], r[None], start=cache.lens, stream=stream)
+        cache.attend(r, 0.05, o, stream=stream)
+        cache.sparse(layer, qb, 0.05, ob, lists=False, stream=stream)
+
+    bufs = lambda: (torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(qb))  # noqa: E731
+    cache.append(kv[0, 0], kv[0, 1], 50)
+    step(*bufs())  # loads the kernels
+    got, graph = bufs(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*got)
+    for i in range(1, 8):
+        cache.append(kv[i, 0], kv[i, 1], 50)
+        graph.replay()
+        want = bufs()
+        step(*want)
+        torch.cuda.synchronize()
+        assert cache.lens.tolist() == [50 * (i + 1)]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert L.losa_get_device_error() == 0

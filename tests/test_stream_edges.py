@@ -47,7 +47,7 @@ def test_lengths_of_captured_and_eager_appends(monkeypatch):
             step()
 
     monkeypatch.setattr(harness, "losa_cache_append", fake)
-    monkeypatch.setattr(harness.torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(harness, "_capturing", lambda t: capturing[0], raising=False)
     cache = harness.KvCache(2, 1, 64, 96, page_tokens=32, device="cpu")
     cache.append(None, None, 5)
     before = cache.lens
@@ -137,3 +137,26 @@ def test_packed_projection_is_allocated_on_the_calls_stream(lib, monkeypatch):
         layer.pack_qkv(torch.zeros(2, 100, 3, 2, 64), None, stream=stream)
         assert seen == [("alloc", [stream]), ("call", stream)]
         seen.clear()
+
+
+def test_lengths_read_by_a_captured_call(monkeypatch):
+    """A graph that only reads the lengths (an attention, a rotation that starts at them) reads them in one place: eager
+    appends behind the capture advance that tensor."""
+    from free_block_sparse_losa_b200 import harness
+    capturing, read = [False], []
+    monkeypatch.setattr(harness, "_capturing", lambda t: capturing[0], raising=False)
+    monkeypatch.setattr(harness, "losa_cache_append",
+                        lambda c, k, v, k8, v8, ks, vs, table, lens, new, new_lens=None, **kw: new_lens.copy_(lens + new))
+    monkeypatch.setattr(harness, "losa_cache_attn", lambda c, q, k8, v8, ks, vs, table, lens, *a, **kw: read.append(lens))
+    monkeypatch.setattr(harness, "losa_cache_sparse_attn", lambda s, c, q, k8, v8, ks, vs, table, lens, *a, **kw: read.append(lens))
+    q = torch.zeros(2, 1, 1, 64)
+    layer = type("Layer", (), dict(shape=None, indptr=None, kv_idx=None, order=None))
+    for use in (lambda c: c.attend(q, 0.1, q), lambda c: c.sparse(layer, q, 0.1, q), lambda c: read.append(c.lens)):
+        cache = harness.KvCache(2, 1, 64, 96, page_tokens=32, device="cpu")
+        cache.append(None, None, 5)
+        capturing[0] = True
+        use(cache)
+        capturing[0] = False
+        for n in (8, 11, 14):
+            cache.append(None, None, 3)
+            assert read[-1].tolist() == cache.lens.tolist() == [n, n] and cache.max_len == n
